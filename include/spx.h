@@ -332,6 +332,87 @@ SPX_API spx_status spx_sparse_mla_attn_fp8(const spx_dims* d, int32_t rows, cons
                                            spx_stream stream);
 
 /* ---------------------------------------------------------------------------
+ * 4-bit latent cache.  [W1] section "양자화: W8A8와 혼합 캐시" keeps cache
+ * entries in 8 bits; the 4-bit form is an addition of this library: 272 bytes
+ * a token instead of 1024 (bf16) or 516 (FP8).  A 512-wide latent row x is
+ * stored as E2M1 codes (sign, two exponent bits with bias 1, one fraction
+ * bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) of x / 2^e, with one exponent e for each
+ * group of 32 dims.  With nat_g the smallest integer such that
+ * max |x_g| <= 6 * 2^nat_g (minus infinity for a group of zeros),
+ *     E   = max_g nat_g, clamped to [-50, 50],
+ *     e_g = nat_g, clamped to [E - 15, E],
+ *     code = the E2M1 value nearest to x / 2^e_g (ties to even, at most 6).
+ * A dequantised row (code value * 2^e_g) is exact in bf16.  Infinities are
+ * stored as the largest value; a group that holds a NaN reads back as NaN.
+ *
+ *   codes   uint8 [.., 256]  dim 2j in the low half of byte j, 2j + 1 in the high
+ *   scales  uint8 [.., 16]   e_g + 127 (255: NaN)       (both 16-byte aligned)
+ *
+ * spx_latent_append_fp4 writes new rows behind those a sequence has: row i of
+ * sequence b goes to position len_dev[b] + i of its cache.  Rows
+ * i >= n_add[b] (a padded batch) and rows whose position lies outside
+ * [0, max_len) are not written.
+ *   latent    bf16 [B, n_new, 512]
+ *   n_add     DEVICE int32 [B] or NULL (n_new rows for every sequence)
+ *   codes, scales   uint8 [B, cap_tok, 256], [B, cap_tok, 16]
+ *   len_dev   DEVICE int64 [B]; the caller advances it afterwards
+ *   max_len   host bound on the lengths after the call, <= cap_tok
+ *   stored    bf16 [B, n_new, 512] or NULL: the written rows as the cache now
+ *             holds them (may be latent itself); other rows are left alone
+ *
+ * spx_latent_read_fp4 reads rows back, dequantised: out[b][i] is the token at
+ * position pos[b][i] of sequence b (pos NULL: position i), or zeros where that
+ * lies outside [0, min(n_vis[b], cap_tok)).  Positions may repeat.
+ *   pos       DEVICE int64 [B, m] or NULL
+ *   n_vis     DEVICE int64 [B]
+ *   out       bf16 [B, m, 512]
+ *
+ * spx_sparse_mla_attn_fp4 is step 4 over such a cache: the attended set and
+ * the result of spx_sparse_mla_attn, the latent rows read as their
+ * dequantised values (rows are dequantised on the way to the tensor cores;
+ * no copy of them is made).  Row r reads token r * seq_stride / 512 + t of
+ * the cache (seq_stride counts latent elements, as for the other caches: a
+ * multiple of 512, at least 512 * cap_tok; 0: a shared cache).  ws:
+ * spx_attn_fp4_workspace_size bytes.
+ *
+ * spx_latent_attn_fp4 attends to every visible token instead of a selection:
+ * row r sees tokens 0 .. n_vis[r] - 1 of sequence r / rows_per_seq, so the
+ * rows_per_seq rows of a sequence (draft tokens, a short causal chunk) share
+ * its cache [rows / rows_per_seq, cap_tok, ..].  Other arguments as above;
+ * ws: spx_latent_attn_fp4_workspace_size bytes for the same rows,
+ * rows_per_seq and max_len.
+ *
+ * A row that sees no token gives out = 0 and lse = -inf.  The queries are
+ * expected to be finite.  The cache arrays may be pinned host memory mapped
+ * into the device's address space.  A workspace belongs to one call at a
+ * time; calls that may overlap on the GPU need one each.
+ * ------------------------------------------------------------------------- */
+SPX_API spx_status spx_latent_append_fp4(int32_t B, const void* latent, int64_t n_new,
+                                         const int32_t* n_add, void* codes, void* scales,
+                                         int64_t cap_tok, const int64_t* len_dev,
+                                         int64_t max_len, void* stored, spx_stream stream);
+SPX_API spx_status spx_latent_read_fp4(int32_t B, const void* codes, const void* scales,
+                                       int64_t cap_tok, const int64_t* pos, int64_t m,
+                                       const int64_t* n_vis, void* out, spx_stream stream);
+SPX_API spx_status spx_attn_fp4_workspace_size(const spx_dims* d, int32_t rows,
+                                               int64_t max_len, size_t* bytes);
+SPX_API spx_status spx_sparse_mla_attn_fp4(const spx_dims* d, int32_t rows, const void* q,
+                                           const void* codes, const void* scales,
+                                           int64_t seq_stride, int64_t cap_tok,
+                                           const int32_t* idx, const int32_t* count,
+                                           const int64_t* n_vis, int64_t max_len, void* out,
+                                           float* lse, void* ws, size_t ws_bytes,
+                                           spx_stream stream);
+SPX_API spx_status spx_latent_attn_fp4_workspace_size(const spx_dims* d, int32_t rows,
+                                                      int32_t rows_per_seq, int64_t max_len,
+                                                      size_t* bytes);
+SPX_API spx_status spx_latent_attn_fp4(const spx_dims* d, int32_t rows, int32_t rows_per_seq,
+                                       const void* q, const void* codes, const void* scales,
+                                       int64_t cap_tok, const int64_t* n_vis, int64_t max_len,
+                                       void* out, float* lse, void* ws, size_t ws_bytes,
+                                       spx_stream stream);
+
+/* ---------------------------------------------------------------------------
  * Step 4 with the latent cache in host memory and a device working set.
  * [W3] "HiSparse는 전체 이력을 GPU 밖으로 옮긴다": the full history stays in
  * host memory, recently used entries stay on the GPU, and a step fetches only

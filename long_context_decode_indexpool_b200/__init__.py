@@ -78,6 +78,15 @@ _SIGS = {
     "spx_attn_fp8_workspace_size": ([_DIMS, _I32, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
     "spx_sparse_mla_attn_fp8": ([_DIMS, _I32, _P, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P, _P,
                                  _SZ, _P], ctypes.c_int),
+    "spx_latent_append_fp4": ([_I32, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P], ctypes.c_int),
+    "spx_latent_read_fp4": ([_I32, _P, _P, _I64, _P, _I64, _P, _P, _P], ctypes.c_int),
+    "spx_attn_fp4_workspace_size": ([_DIMS, _I32, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "spx_sparse_mla_attn_fp4": ([_DIMS, _I32, _P, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P, _P,
+                                 _SZ, _P], ctypes.c_int),
+    "spx_latent_attn_fp4_workspace_size": ([_DIMS, _I32, _I32, _I64, ctypes.POINTER(_SZ)],
+                                           ctypes.c_int),
+    "spx_latent_attn_fp4": ([_DIMS, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P],
+                            ctypes.c_int),
     "spx_ws_workspace_size": ([_DIMS, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
     "spx_sparse_mla_attn_ws": ([_DIMS, _I32, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P, _I32, _P, _P,
                                 _P, _P, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
@@ -280,6 +289,57 @@ def spx_sparse_mla_attn_fp8(d, rows, q, codes, exps, seq_stride, cap_tok, idx, c
                                         seq_stride, cap_tok, _ptr(idx), _ptr(count), _ptr(n_vis),
                                         max_len, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
                                         _stream(stream)), "spx_sparse_mla_attn_fp8")
+
+
+def spx_latent_append_fp4(B, latent, n_new, n_add, codes, scales, cap_tok, len_dev, max_len,
+                          stored=None, stream=None):
+    """Quantising write of new latent rows behind each sequence's cached ones."""
+    _check(_lib.spx_latent_append_fp4(B, _ptr(latent), n_new, _ptr(n_add), _ptr(codes),
+                                      _ptr(scales), cap_tok, _ptr(len_dev), max_len, _ptr(stored),
+                                      _stream(stream)), "spx_latent_append_fp4")
+
+
+def spx_latent_read_fp4(B, codes, scales, cap_tok, pos, m, n_vis, out, stream=None):
+    """Rows of the 4-bit latent cache, dequantised (pos None: the first m of each sequence)."""
+    _check(_lib.spx_latent_read_fp4(B, _ptr(codes), _ptr(scales), cap_tok, _ptr(pos), m,
+                                    _ptr(n_vis), _ptr(out), _stream(stream)),
+           "spx_latent_read_fp4")
+
+
+def spx_attn_fp4_workspace_size(d, rows, max_len) -> int:
+    n = _SZ(0)
+    _check(_lib.spx_attn_fp4_workspace_size(ctypes.byref(d), rows, max_len, ctypes.byref(n)),
+           "spx_attn_fp4_workspace_size")
+    return n.value
+
+
+def spx_sparse_mla_attn_fp4(d, rows, q, codes, scales, seq_stride, cap_tok, idx, count, n_vis,
+                            max_len, out, lse=None, ws=None, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(_lib.spx_sparse_mla_attn_fp4(ctypes.byref(d), rows, _ptr(q), _ptr(codes), _ptr(scales),
+                                        seq_stride, cap_tok, _ptr(idx), _ptr(count), _ptr(n_vis),
+                                        max_len, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                        _stream(stream)), "spx_sparse_mla_attn_fp4")
+
+
+def spx_latent_attn_fp4_workspace_size(d, rows, rows_per_seq, max_len) -> int:
+    n = _SZ(0)
+    _check(_lib.spx_latent_attn_fp4_workspace_size(ctypes.byref(d), rows, rows_per_seq, max_len,
+                                                   ctypes.byref(n)),
+           "spx_latent_attn_fp4_workspace_size")
+    return n.value
+
+
+def spx_latent_attn_fp4(d, rows, rows_per_seq, q, codes, scales, cap_tok, n_vis, max_len, out,
+                        lse=None, ws=None, ws_bytes=None, stream=None):
+    """Attention of each row over every token it sees in the 4-bit latent cache."""
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(_lib.spx_latent_attn_fp4(ctypes.byref(d), rows, rows_per_seq, _ptr(q), _ptr(codes),
+                                    _ptr(scales), cap_tok, _ptr(n_vis), max_len, _ptr(out),
+                                    _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)),
+           "spx_latent_attn_fp4")
 
 
 def spx_ws_workspace_size(d, rows, nslots) -> int:

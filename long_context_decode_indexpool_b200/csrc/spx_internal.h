@@ -189,6 +189,38 @@ cudaError_t launch_gather_fp8(int rows, const uint8_t* codes, const int32_t* exp
                               int64_t dense_stride, int32_t* c_idx, int32_t* c_cnt,
                               int64_t* c_nvis, cudaStream_t stream);
 
+// 4-bit (E2M1) latent cache (latent_fp4.cuh has the format): codes
+// [.., 256] and group scale bytes [.., 16] per token.  latent_fp4.cu writes
+// and reads rows, attn_fp4.cu attends over them.
+cudaError_t launch_latent_append_fp4(int B, const void* lat, int64_t n_new, const int32_t* n_add,
+                                     uint8_t* codes, uint8_t* scales, int64_t cap_tok,
+                                     const int64_t* len_dev, int64_t max_len, void* stored,
+                                     cudaStream_t stream);
+cudaError_t launch_latent_read_fp4(int B, const uint8_t* codes, const uint8_t* scales,
+                                   int64_t cap_tok, const int64_t* pos, int64_t m,
+                                   const int64_t* n_vis, void* out, cudaStream_t stream);
+struct AttnFp4Plan {
+  size_t ws_bytes;
+};
+struct AttnFp4Args {
+  int rows, per_seq, heads;  // row r attends to sequence r / per_seq
+  const void* q;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t seq_tok;       // tokens from one sequence to the next (0: one cache)
+  int64_t len_cap;       // min(max_len, cap_tok)
+  const int32_t* idx;    // selected blocks [rows, 512] and their counts, or
+  const int32_t* count;  // null: every visible token
+  const int64_t* n_vis;
+  float sm_scale;
+  void* out;
+  float* lse;
+  void* ws;
+};
+AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t max_len,
+                          int num_sms);
+cudaError_t launch_attn_fp4(const AttnFp4Plan& p, const AttnFp4Args& a, cudaStream_t stream);
+
 // Device working set of a host-resident latent cache (working_set.cu): the
 // per-step hit/miss pass and the fetch of the missed blocks and tail tokens
 // into the slot pool [rows, nslots + 1, 4, 512].

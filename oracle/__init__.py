@@ -67,6 +67,12 @@ def _load():
             lib.orc_e4m3_value.restype = ctypes.c_double
             lib.orc_quant_e4m3.argtypes = [P, ctypes.c_int, P]
             lib.orc_quant_e4m3.restype = ctypes.c_int
+            lib.orc_e2m1_code.argtypes = [ctypes.c_double]
+            lib.orc_e2m1_code.restype = ctypes.c_uint8
+            lib.orc_e2m1_value.argtypes = [ctypes.c_uint8]
+            lib.orc_e2m1_value.restype = ctypes.c_double
+            lib.orc_quant_e2m1.argtypes = [P, ctypes.c_int, P, P]
+            lib.orc_quant_e2m1.restype = None
             lib.orc_topk.argtypes = [P, i64, i64, P]
             lib.orc_topk.restype = i64
             lib.orc_token_set.argtypes = [P, i64, i64, ctypes.c_int, P]
@@ -206,6 +212,48 @@ def dequant_fp8_bits(codes: np.ndarray, e) -> np.ndarray:
     bits = np.array([bf16_rne(v) for v in vals.reshape(-1)], dtype=np.uint16).reshape(vals.shape)
     assert np.array_equal(bf16_to_f64(bits), vals)
     return bits
+
+
+def e2m1_code(v: float) -> int:
+    """E2M1 code (0..15) of the nearest-even E2M1 value of v."""
+    return int(_load().orc_e2m1_code(float(v)))
+
+
+def e2m1_value(codes) -> np.ndarray:
+    """Values (fp64) of E2M1 codes."""
+    lib = _load()
+    table = np.array([lib.orc_e2m1_value(c) for c in range(16)], dtype=np.float64)
+    return table[np.asarray(codes, dtype=np.uint8)]
+
+
+def latent_fp4(rows_bits: np.ndarray):
+    """4-bit latent cache of bf16 latent rows [S, D]: (codes [S, D/2] uint8 with
+    the even dim in the low half, scale bytes [S, D/32] uint8)."""
+    rows = np.ascontiguousarray(bf16_to_f64(rows_bits)).reshape(-1, np.shape(rows_bits)[-1])
+    S, D = rows.shape
+    nib = np.zeros((S, D), dtype=np.uint8)
+    scales = np.zeros((S, D // 32), dtype=np.uint8)
+    for i in range(S):
+        _load().orc_quant_e2m1(_p(rows[i]), D, _p(nib[i]), _p(scales[i]))
+    return nib[:, 0::2] | (nib[:, 1::2] << 4), scales
+
+
+def dequant_fp4(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """Rows [S, D] (fp64) of a 4-bit latent cache; NaN where a scale byte is 255."""
+    codes = np.asarray(codes, dtype=np.uint8)
+    nib = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)
+    sb = np.asarray(scales, dtype=np.uint8).astype(np.int64)
+    s = np.where(sb == 255, np.nan, np.ldexp(1.0, np.where(sb == 255, 0, sb - 127)))
+    return e2m1_value(nib) * np.repeat(s, 32, -1)
+
+
+def attention_fp4(q_bits: np.ndarray, codes: np.ndarray, scales: np.ndarray, sm_scale: float):
+    """Attention of q [H, D] over the rows of a 4-bit latent cache (finite
+    rows: their values are exact in bf16)."""
+    vals = dequant_fp4(codes, scales)
+    bits = (vals.astype(np.float32).view(np.uint32) >> np.uint32(16)).astype(np.uint16)
+    assert np.array_equal(bf16_to_f64(bits), vals)
+    return attention(q_bits, bits, sm_scale)
 
 
 def topk(scores, K: int = TOPK_BLOCKS) -> np.ndarray:

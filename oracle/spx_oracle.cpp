@@ -285,6 +285,64 @@ int orc_quant_e4m3(const double* x, int n, uint8_t* codes) {
   return e;
 }
 
+// ---- 4-bit (E2M1) latent cache -------------------------------------------------
+// Codes: sign, two exponent bits with bias 1, one fraction bit; one exponent
+// per group of 32 values.  nat = the smallest integer with max |x| <= 6 * 2^nat;
+// the row's exponent E is the largest nat, clamped to [-50, 50]; a group's
+// exponent is its nat clamped to [E - 15, E].
+
+// Value of an E2M1 code.
+double orc_e2m1_value(uint8_t code) {
+  static const double mag[8] = {0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0};
+  return (code & 8) ? -mag[code & 7] : mag[code & 7];
+}
+
+// Code of the E2M1 value nearest to v: of two equally near the one whose last
+// bit is 0; magnitudes above 6 give 6.
+uint8_t orc_e2m1_code(double v) {
+  const double a = std::fabs(v);
+  int best = 0;
+  if (a >= 6.0) {
+    best = 7;
+  } else {
+    for (int c = 1; c < 8; ++c) {
+      const double d = std::fabs(a - orc_e2m1_value(c)), db = std::fabs(a - orc_e2m1_value(best));
+      if (d < db || (d == db && (c & 1) == 0)) best = c;
+    }
+  }
+  return static_cast<uint8_t>(best | (std::signbit(v) ? 8 : 0));
+}
+
+// One row of n values (a multiple of 32): codes, one per value, and the scale
+// bytes e + 127 of its groups (255 for a group that holds a NaN).
+void orc_quant_e2m1(const double* x, int n, uint8_t* codes, uint8_t* scales) {
+  const int ng = n / 32;
+  std::vector<int> nat(ng);
+  std::vector<bool> bad(ng);
+  int E = -50;
+  for (int g = 0; g < ng; ++g) {
+    double amax = 0.0;
+    bad[g] = false;
+    for (int i = 0; i < 32; ++i) {
+      if (std::isnan(x[32 * g + i])) bad[g] = true;
+      amax = std::max(amax, std::fabs(x[32 * g + i]));
+    }
+    nat[g] = -1000;
+    if (amax > 0.0) {
+      nat[g] = std::isinf(amax) ? 1000 : std::ilogb(amax) + 1;
+      while (!std::isinf(amax) && amax <= std::ldexp(6.0, nat[g] - 1)) --nat[g];
+    }
+    if (!bad[g]) E = std::max(E, nat[g]);
+  }
+  E = std::min(E, 50);
+  for (int g = 0; g < ng; ++g) {
+    const int e = std::min(std::max(nat[g], E - 15), E);
+    scales[g] = static_cast<uint8_t>(bad[g] ? 255 : e + 127);
+    for (int i = 0; i < 32; ++i)
+      codes[32 * g + i] = bad[g] ? 0 : orc_e2m1_code(std::ldexp(x[32 * g + i], -e));
+  }
+}
+
 // Top-k block selection [W4 "수렴점 2": keep the 512 highest-scoring 4-token
 // blocks]: full sort on (score descending, block ascending) -- equal scores
 // go to the lower block index -- keep the first min(K, nblk), return them
