@@ -1,144 +1,930 @@
-// Latent attention over a cache held in 4 bits (format: latent_fp4.cuh):
+// Latent attention over a cache held in 4 bits (format: latent_fp4.cuh), on
+// the 5th-generation tensor cores:
 //   out[h] = sum_t softmax_t(sm_scale * q_h . c_t) c_t   over a token set S,
-// S either the tokens of the row's selected blocks and its partial tail, or
-// every token the row sees.
+// S either the tokens of the row's selected blocks and its partial tail
+// (spx_sparse_mla_attn_fp4), or every token the row sees
+// (spx_latent_attn_fp4).
 //
-// One CTA takes one row and 16 heads: tiles of 32 tokens are dequantised into
-// shared memory (fp32), the running maximum and sum of each head are kept in
-// fp32, and each thread owns two dims of every head's output.
+// Operands.  A cached row is c_t = 2^E_t c'_t, E_t its largest group exponent
+// and c'_t exact in fp16; a query head is q_h = 2^-s_h q'_h with max |q'_h| in
+// [2^14, 2^15), exact in fp16 down to 2^-32 of that.  So
+//   z_t = log2(e) sm_scale 2^-s_h 2^E_t (q'_h . c'_t) + E_t   (base 2),
+//   P_t = 2^(z_t - R),  O = sum_t P_t c'_t,  l = sum_t P_t 2^-E_t,
+//   out = O / l,  lse = (R + log2 l) ln 2.
+// The running maximum is taken of z, the size of a token's contribution to O,
+// not of the logit alone, so P fits fp16 (11 bits where bf16 has 8: the
+// output's error is then its own rounding, not P's) whatever the rows'
+// exponents; R is the maximum less 7, so P's subnormals begin 2^21 below the
+// largest term, and the maximum is raised lazily (at most 2^15 in all).  l is
+// a sum of unrounded fp32 values.
+//
+// Work.  A unit is 64 (row, head) pairs that share a token list: 64 heads of
+// a row, or, with fewer heads, several rows of a sequence.  All units' lists,
+// in tiles of 64 tokens, form one sequence of tiles that is cut into equal
+// parts, one per CTA (one CTA per SM), whatever the lengths.  A CTA walks its
+// part as segments of units; a segment that is not its whole unit leaves its
+// O and (R, l) in fp32 in the workspace, and k_attn_fp4_combine joins them.
+//
+// One CTA: 8 worker warps (softmax, output), one MMA warp, 7 converter warps.
+// TMEM (an M = 64 accumulator puts row 16w+i in lane 32w+i, or 32w+16+i with
+// the lane offset 16):
+//   O dims   0-255: lanes 32w+i,    columns 0-255
+//   O dims 256-511: lanes 32w+16+i, columns 0-255
+//   S (64 tokens):  lanes 32w+16+i, columns 256+64b .. (b = S buffer 0/1)
+// Converter warps take groups of 8 tokens in turn (codes and scales are
+// loaded one group ahead, block ids two), multiply the codes up to fp16 in
+// registers and store them in the 128-byte-swizzle layout, double-buffered: a
+// buffer is refilled as soon as the PV of its previous tile is done.  The MMA
+// warp issues S = Q C^T (M = 64, N = 64, K = 16, 32 times) and O += P C (M =
+// 64, N = 256, K = 16, 8 times, C read MN-major from the same tile), whichever
+// is ready first.  A worker warp shares a TMEM lane quarter with another; each
+// takes 32 of a tile's tokens, the two threads of lanes i and 16+i a head.
+#include <atomic>
+
 #include "latent_fp4.cuh"
 #include "spx_device.cuh"
 #include "spx_internal.h"
+#include "spx_launch.cuh"
 
 namespace spx {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 32;
-constexpr int kHeads = 16;
-constexpr int kSmem = (kTile * kLatent + kHeads * kLatent) * 4;
+constexpr int kWork = 256;       // worker threads (warps 0-7)
+constexpr int kMmaWarp = 8;
+constexpr int kConvWarp0 = 9;
+constexpr int kConvWarps = 7;    // 16 warps in all: 128 registers a thread
+constexpr int kThreads = (kConvWarp0 + kConvWarps) * 32;
+constexpr int kTT = 64;          // tokens per tile
+constexpr int kM = 64;           // (row, head) pairs per unit (MMA M)
+constexpr int kOct = 8;          // tokens a converter warp takes at a time
+constexpr int kOcts = kTT / kOct;
+constexpr int kRegion = 64 * 128;        // [64 rows x 128 B] = 8 KiB
+constexpr int kQBytes = 8 * kRegion;     // 64 KiB
+constexpr int kKVRegion = 2 * kRegion;   // both latent buffers, 64 dims
+constexpr int kKVBytes = 8 * kKVRegion;  // 128 KiB
+constexpr int kPBytes = kRegion;         // [64 x 64 tokens] fp16, two buffers
+constexpr int kSmemBytes = 1024 + kQBytes + kKVBytes + 2 * kPBytes;
+constexpr float kLazy = 8.f;   // the maximum is raised when exceeded by more
+constexpr float kLift = 7.f;   // P = 2^(z - max + 7)
+constexpr int kMaxGrid = 160;  // CTAs (one per SM, at most)
+constexpr int kPartFloats = kM * kLatent;
+constexpr uint32_t kIdescF16 = (1u << 4) | (static_cast<uint32_t>(kM >> 4) << 24);  // f16 A, B; f32 D
+constexpr uint32_t kIdescPV = kIdescF16 | ((256u >> 3) << 17) | (1u << 16);  // B MN-major
+static_assert(kSmemBytes + 6 * 1024 <= 232448, "shared memory budget");
 
-__global__ void __launch_bounds__(kThreads) k_attn_fp4(const AttnFp4Args a) {
-  extern __shared__ float sm[];
-  float* c_s = sm;                    // [kTile][512]
-  float* q_s = sm + kTile * kLatent;  // [16][512]
-  __shared__ float z_s[kHeads][kTile], corr_s[kHeads], m_s[kHeads], l_s[kHeads];
-  __shared__ int64_t pos_s[kTile];
-  const int r = blockIdx.x, h0 = blockIdx.y * kHeads, tid = threadIdx.x;
-  int64_t n = a.n_vis[r];
-  n = n < 0 ? 0 : (n > a.len_cap ? a.len_cap : n);
-  const int64_t nblk = n / kPool;
-  int64_t S = n;
-  int cnt = 0;
-  if (a.idx) {
-    cnt = min(max(a.count[r], 0), kTopK);
-    if (cnt > nblk) cnt = static_cast<int>(nblk);
-    S = cnt * kPool + (n - nblk * kPool);
+struct KParams {
+  const __nv_bfloat16* q;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t seq_tok;
+  int64_t len_cap;
+  const int32_t* idx;
+  const int32_t* count;
+  const int64_t* n_vis;
+  int heads, per_seq;
+  int units, groups;       // groups of 64 heads per row (dense: or rgs > 1)
+  int rows_per_unit, rgs;  // rows of a unit; units per (sequence, head group)
+  int min_tiles;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  int2* comb;      // [grid] (unit, CTAs it spans) of the split unit that begins in a CTA
+  float2* part_ml; // [2 grid][64] (R, l)
+  float4* part_o;  // [2 grid][32 pieces][256 worker threads]
+};
+
+// A tile as its converters describe it to the other roles.
+struct TileMeta {
+  int ntok;   // tokens in its list part (0..64)
+  int unit;
+  int tile;   // index in the unit
+  int flags;
+};
+enum : int { kFirst = 1, kLast = 2, kHead = 4, kTail = 8 };  // of the segment; of the unit
+
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void pair_sync(int qd) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte-swizzle
+// layout: 64-element groups along MN `lbo` bytes apart, 8-row groups along K
+// `sbo` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
+      "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
+      "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
+      "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
+      "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
+      "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ---- units --------------------------------------------------------------------
+__device__ __forceinline__ int clamp_len(const KParams& p, int64_t row) {
+  const int64_t n = p.n_vis[row];
+  return static_cast<int>(n < 0 ? 0 : (n > p.len_cap ? p.len_cap : n));
+}
+
+// First row of unit u and its head group; rows u holds.
+struct UnitRows {
+  int row0, nrows, hg;
+};
+template <bool kSparse>
+__device__ __forceinline__ UnitRows unit_rows(const KParams& p, int u) {
+  UnitRows r;
+  const int rest = u / p.groups;
+  r.hg = u - rest * p.groups;
+  if (kSparse) {
+    r.row0 = rest;
+    r.nrows = 1;
+  } else {
+    const int s = rest / p.rgs, rg = rest - s * p.rgs;
+    r.row0 = s * p.per_seq + rg * p.rows_per_unit;
+    r.nrows = min(p.rows_per_unit, p.per_seq - rg * p.rows_per_unit);
   }
-  const int64_t base = static_cast<int64_t>(r / a.per_seq) * a.seq_tok;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                           (static_cast<int64_t>(r) * a.heads + h0) * kLatent;
-  for (int i = tid; i < kHeads * kLatent; i += kThreads) q_s[i] = __bfloat162float(q[i]);
-  if (tid < kHeads) {
-    m_s[tid] = -INFINITY;
-    l_s[tid] = 0.f;
+  return r;
+}
+
+struct Unit {
+  int n, cnt, S;  // visible tokens, selected blocks, tokens in the list
+};
+template <bool kSparse>
+__device__ __forceinline__ Unit load_unit(const KParams& p, int u) {
+  Unit x;
+  const UnitRows r = unit_rows<kSparse>(p, u);
+  x.n = clamp_len(p, r.row0);
+  if (kSparse) {
+    const int c = p.count[r.row0];
+    x.cnt = min(min(max(c, 0), kTopK), x.n / kPool);
+    x.S = x.cnt * kPool + (x.n & (kPool - 1));
+  } else {
+    for (int i = 1; i < r.nrows; ++i) x.n = max(x.n, clamp_len(p, r.row0 + i));
+    x.cnt = 0;
+    x.S = x.n;
   }
-  float o[kHeads][2];
-  for (int h = 0; h < kHeads; ++h) o[h][0] = o[h][1] = 0.f;
-  for (int64_t t0 = 0; t0 < S; t0 += kTile) {
+  return x;
+}
+// A unit without tokens still has one tile: its rows' outputs are written.
+__device__ __forceinline__ int tiles_of(int S) { return max(1, (S + kTT - 1) / kTT); }
+
+// The part of the tile sequence a CTA owns, as every thread learns it.
+struct Part {
+  int64_t begin, end, quota;
+  int u0;        // unit of tile `begin`
+  int64_t off0;  // first tile of that unit
+};
+
+// Scans the units' tile counts (every thread of the block calls this).
+template <bool kSparse>
+__device__ Part plan_part(const KParams& p, int64_t* scratch /* [20] */) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Part part;
+  int64_t sum = 0;
+  int first = 0;  // tiles of unit tid, kept for the scan
+  for (int u = tid; u < p.units; u += kThreads) {
+    const int t = tiles_of(load_unit<kSparse>(p, u).S);
+    if (u == tid) first = t;
+    sum += t;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
+  __syncthreads();
+  const int64_t g = gridDim.x;
+  part.quota = max((total + g - 1) / g, static_cast<int64_t>(p.min_tiles));
+  part.begin = part.quota * blockIdx.x;
+  part.end = min(part.begin + part.quota, total);
+  part.u0 = 0;
+  part.off0 = 0;
+  int64_t base = 0;
+  for (int b = 0; part.begin < total; b += kThreads) {  // uniform; ends where the unit is found
+    const int u = b + tid;
+    int64_t t = 0;
+    if (u < p.units) t = b == 0 ? first : tiles_of(load_unit<kSparse>(p, u).S);
+    int64_t inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
     __syncthreads();
-    if (tid < kTile) {
-      int64_t p = -1;
-      if (t0 + tid < S) {
-        p = t0 + tid;
-        if (a.idx) {
-          if (p < cnt * kPool) {
-            const int b = a.idx[static_cast<int64_t>(r) * kTopK + (p >> 2)];
-            p = b < 0 || b >= nblk ? -1 : static_cast<int64_t>(b) * kPool + (p & 3);
-          } else {
-            p = nblk * kPool + (p - cnt * kPool);
+    int64_t before = base, all = base;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scratch[w];
+      all += scratch[w];
+    }
+    const int64_t off = before + inc - t;
+    if (t > 0 && off <= part.begin && part.begin < off + t) {
+      scratch[16] = u;
+      scratch[17] = off;
+    }
+    __syncthreads();
+    if (part.begin < all) {
+      part.u0 = static_cast<int>(scratch[16]);
+      part.off0 = scratch[17];
+      break;
+    }
+    base = all;
+    if (b + kThreads >= p.units) break;  // (cannot happen: begin < total)
+  }
+  return part;
+}
+
+// ---- queries ------------------------------------------------------------------
+// Rows w, w + nw, .. of the unit's 64 query rows to shared memory as fp16,
+// each scaled by a power of two; hs[m] is what a product with it is multiplied
+// by.  `wait` is called between the first loads and the first store.
+template <bool kSparse, typename Wait>
+__device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t q_u, float* hs, int w,
+                                       int nw, Wait wait) {
+  const int lane = threadIdx.x & 31;
+  const UnitRows r = unit_rows<kSparse>(p, u);
+  const int hpr = min(p.heads, kM);  // heads of a row in the unit
+  bool waited = false;
+#pragma unroll 1
+  for (int m0 = w; m0 < kM; m0 += 4 * nw) {
+    uint4 v[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + i * nw;
+      const int rr = m / hpr, h = r.hg * kM + m - rr * hpr;
+      v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (m < kM && rr < r.nrows && h < p.heads) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<int64_t>(r.row0 + rr) * p.heads + h) * kLatent);
+        v[i][0] = src[lane];
+        v[i][1] = src[32 + lane];
+      }
+    }
+    if (!waited) wait();
+    waited = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + i * nw;
+      if (m >= kM) break;  // uniform
+      const uint32_t mask = 0x7FFF7FFFu;
+      uint32_t a = __vmaxu2(__vmaxu2(v[i][0].x & mask, v[i][0].y & mask),
+                            __vmaxu2(v[i][0].z & mask, v[i][0].w & mask));
+      a = __vmaxu2(a, __vmaxu2(__vmaxu2(v[i][1].x & mask, v[i][1].y & mask),
+                               __vmaxu2(v[i][1].z & mask, v[i][1].w & mask)));
+      const uint32_t big = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
+      const int s = min(14 + 127 - static_cast<int>(big >> 7), 110);
+      const float f = __int_as_float((127 + s) << 23);  // 2^s
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4 x = v[i][half];
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = h2_bits(__floats2half2_rn(__uint_as_float(in[k] << 16) * f,
+                                           __uint_as_float(in[k] & 0xFFFF0000u) * f));
+        const int piece = 32 * half + lane;
+        sts128(q_u + (piece >> 3) * kRegion + m * 128 + (((piece & 7) ^ (m & 7)) << 4), o[0], o[1],
+               o[2], o[3]);
+      }
+      if (lane == 0) hs[m] = p.scale_log2 * __int_as_float((127 - s) << 23);
+    }
+  }
+}
+
+// ---- the kernel -----------------------------------------------------------------
+template <bool kSparse>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
+  extern __shared__ uint8_t dyn[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  const uint32_t q_u = smem_u32(sm), kv_u = q_u + kQBytes, p_u = kv_u + kKVBytes;
+  __shared__ uint64_t bar_qk[2], bar_pv[2], bar_kv[2], bar_p[2], bar_q0, bar_q, bar_drain;
+  __shared__ TileMeta meta_s[4];
+  __shared__ __align__(16) float2 te_s[2][kTT];  // (2^E, E) per token; (1, -inf): nothing there
+  __shared__ float hs_s[4][kM];                  // per segment, mod 4
+  __shared__ float red_m[2][2][kM], red_l[2][kM];
+  __shared__ int64_t scratch[20];
+  __shared__ uint32_t tmem_holder;
+  __shared__ int abort_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_qk[i], 1);
+      mbar_init(&bar_pv[i], 1);
+      mbar_init(&bar_kv[i], kOcts);  // one arrive per group of 8 tokens
+      mbar_init(&bar_p[i], kWork / 32);
+    }
+    mbar_init(&bar_q0, kWork / 32);
+    mbar_init(&bar_q, kConvWarps);
+    mbar_init(&bar_drain, 1);
+    abort_s = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_holder, 512);
+    tmem_relinquish();
+  }
+  pdl_trigger();
+  const Part part = plan_part<kSparse>(p, scratch);
+  const int ntiles = part.begin < part.end ? static_cast<int>(part.end - part.begin) : 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  volatile int* const abort = &abort_s;
+  bool ok = true;
+
+  if (ntiles == 0) {
+    if (tid == 0 && p.comb) p.comb[blockIdx.x] = make_int2(-1, 0);
+  } else if (warp >= kConvWarp0) {
+    // ======================= converter warps ==================================
+    const int w = warp - kConvWarp0;
+    const int nx = ntiles * kOcts;
+    const int r8 = lane & 7, g4 = lane >> 3;
+    // the unit under the cursor, the one after it, and where they end
+    int u = part.u0, t_end, t_org;  // CTA tiles [t_org, t_end) belong to u (t_org may be < 0)
+    Unit un = load_unit<kSparse>(p, u), nxt{};
+    int64_t off = part.off0;
+    t_org = static_cast<int>(off - part.begin);
+    t_end = t_org + tiles_of(un.S);
+    if (u + 1 < p.units) nxt = load_unit<kSparse>(p, u + 1);
+    int2 comb = make_int2(-1, 0);
+
+    // what is known of a group of 8 tokens before its block id arrives
+    struct Req {
+      int b;       // block id (sparse)
+      int fixed;   // the position where no id decides it; -2: the id does
+      int nblk;
+      int seq;     // sequence of the cache
+      TileMeta m;
+    } rq;
+    struct Oct {
+      uint4 c[4], sc;
+      bool valid;
+      TileMeta m;
+    } cur, nx_oct;
+
+    auto request = [&](int x) {  // group x of the CTA; x grows by less than a tile
+      const int t = x >> 3;
+      while (t >= t_end) {  // next unit
+        ++u;
+        un = nxt;
+        t_org = t_end;
+        t_end = t_org + tiles_of(un.S);
+        if (u + 1 < p.units) nxt = load_unit<kSparse>(p, u + 1);
+      }
+      const int tile = t - t_org;
+      const int last = min(t_end, ntiles) - 1;
+      rq.m.unit = u;
+      rq.m.tile = tile;
+      rq.m.ntok = max(0, min(un.S - tile * kTT, kTT));
+      rq.m.flags = ((t == max(t_org, 0)) ? kFirst : 0) | (t == last ? kLast : 0) |
+                   (t_org >= 0 ? kHead : 0) | (t_end <= ntiles ? kTail : 0);
+      if (t_org >= 0 && t_end > ntiles) {  // the split unit that begins here
+        const int64_t last_tile = part.begin + t_end - 1;
+        comb = make_int2(u, static_cast<int>(last_tile / part.quota) -
+                                static_cast<int>(blockIdx.x) + 1);
+      }
+      const int j = tile * kTT + (x & 7) * kOct + r8;
+      const UnitRows ur = unit_rows<kSparse>(p, u);
+      rq.seq = kSparse ? ur.row0 : ur.row0 / p.per_seq;
+      rq.fixed = j < un.S ? j : -1;
+      rq.b = -1;
+      rq.nblk = un.n / kPool;
+      if (kSparse && rq.fixed >= 0) {
+        if (j < un.cnt * kPool) {
+          rq.fixed = -2;
+          rq.b = p.idx[static_cast<int64_t>(ur.row0) * kTopK + (j >> 2)];
+        } else {
+          rq.fixed = rq.nblk * kPool + (j - un.cnt * kPool);
+        }
+      }
+    };
+    auto load = [&](Oct& o) {  // the codes and scales of the requested group
+      int pos = rq.fixed;
+      if (kSparse && pos == -2) pos = rq.b < 0 || rq.b >= rq.nblk ? -1 : rq.b * kPool + (r8 & 3);
+      o.m = rq.m;
+      o.valid = pos >= 0;
+      o.sc = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o.c[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (o.valid) {
+        const int64_t at = static_cast<int64_t>(rq.seq) * p.seq_tok + pos;
+        o.sc = *reinterpret_cast<const uint4*>(p.scales + at * kFp4Groups);
+        const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * kFp4CodeBytes);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o.c[k] = src[4 * k + g4];
+      }
+    };
+    auto convert = [&](const Oct& o, int x) {
+      const int t = x >> 3, oct = x & 7, buf = t & 1;
+      if (t >= 2) ok &= mbar_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
+      if (oct == 0 && lane == 0) meta_s[t & 3] = o.m;
+      // the row's largest exponent byte but 255 (a NaN group): bytes + 1 mod
+      // 256, a word of four per lane
+      const uint32_t sw[4] = {o.sc.x, o.sc.y, o.sc.z, o.sc.w};
+      const uint32_t mine = g4 < 2 ? (g4 == 0 ? sw[0] : sw[1]) : (g4 == 2 ? sw[2] : sw[3]);
+      uint32_t mx = __vmaxu2(((mine & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu,
+                             (((mine >> 8) & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      // biased exponent of the row, kept where 2^E and 2^-E are normal
+      const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
+      const int row = oct * kOct + r8;
+      if (lane < kOct)
+        te_s[buf][row] = o.valid ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
+                                 : make_float2(1.f, -INFINITY);
+      // tokens up to the next multiple of 16 take part in the products
+      if (oct * kOct < max(16, (o.m.ntok + 15) & ~15)) {
+        const uint32_t base = kv_u + (buf * kTT + row) * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int g = 4 * k + g4;
+          const int b = static_cast<int>((sw[k] >> (8 * g4)) & 0xFFu);
+          // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group)
+          __half s = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
+          if (b == kFp4NanByte) s = __ushort_as_half(0x7E00);
+          const __half2 s2 = __half2half2(s);
+          const uint32_t in[4] = {o.c[k].x, o.c[k].y, o.c[k].z, o.c[k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = h2_bits(__hmul2(fp4x2_to_half2(in[i] >> (8 * e)), s2));
+            sts128(base + (g >> 1) * kKVRegion + (((4 * (g & 1) + i) ^ r8) << 4), v[0], v[1], v[2],
+                   v[3]);
           }
         }
       }
-      pos_s[tid] = p;
-    }
-    __syncthreads();
-    for (int i = tid; i < kTile * (kLatent / 2); i += kThreads) {
-      const int t = i / (kLatent / 2), j = i % (kLatent / 2);
-      float2 f = make_float2(0.f, 0.f);
-      if (pos_s[t] >= 0) {
-        const int64_t at = base + pos_s[t];
-        const float s = fp4_scale(a.scales[at * kFp4Groups + j / 16]);
-        f = __half22float2(fp4x2_to_half2(a.codes[at * kFp4CodeBytes + j]));
-        f.x *= s;
-        f.y *= s;
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_kv[buf]);
+    };
+
+    int seg = 0, seg_tile = 0;  // segments begun, first tile of the current one
+    request(w);
+    load(cur);
+    if (w + kConvWarps < nx) request(w + kConvWarps);
+#pragma unroll 1
+    for (int x = w; x < nx; x += kConvWarps) {
+      if (x + kConvWarps < nx) {
+        load(nx_oct);
+        if (x + 2 * kConvWarps < nx) request(x + 2 * kConvWarps);
       }
-      c_s[t * kLatent + 2 * j] = f.x;
-      c_s[t * kLatent + 2 * j + 1] = f.y;
-    }
-    __syncthreads();
-    for (int i = tid; i < kHeads * kTile; i += kThreads) {
-      const int h = i / kTile, t = i % kTile;
-      float s = 0.f;
-      for (int d = 0; d < kLatent; ++d) {
-        const int k = (d + t) & (kLatent - 1);  // lanes on different banks
-        s += q_s[h * kLatent + k] * c_s[t * kLatent + k];
+      const int t = x >> 3;
+      if ((cur.m.flags & kFirst) && t > seg_tile) {
+        // this warp's first group of a later segment: its share of the new
+        // queries, once the last product with the old ones is done (and
+        // before its arrival for the tile, which publishes hs_s to the
+        // workers)
+        seg_tile = t;
+        ++seg;
+        load_q<kSparse>(p, cur.m.unit, q_u, hs_s[seg & 3], w, kConvWarps, [&] {
+          ok &= mbar_wait(&bar_qk[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
+        });
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q);
       }
-      z_s[h][t] = pos_s[t] >= 0 ? s * a.sm_scale : -INFINITY;
+      convert(cur, x);
+      cur = nx_oct;
     }
-    __syncthreads();
-    if (tid < kHeads) {
-      float m = m_s[tid];
-      for (int t = 0; t < kTile; ++t) m = fmaxf(m, z_s[tid][t]);
-      const float corr = m_s[tid] == -INFINITY ? 0.f : expf(m_s[tid] - m);
-      float l = l_s[tid] * corr;
-      for (int t = 0; t < kTile; ++t) {
-        const float p = z_s[tid][t] == -INFINITY ? 0.f : expf(z_s[tid][t] - m);
-        z_s[tid][t] = p;
-        l += p;
+    if (w == 0 && lane == 0 && p.comb) p.comb[blockIdx.x] = comb;
+  } else if (warp == kMmaWarp) {
+    // ======================= MMA issuer =======================================
+    // The whole warp runs the loop (lane 0 polls the barriers and broadcasts
+    // the decision), so the descriptors are warp-uniform.
+    int nq = 0, np = 0, seg = 0;  // tiles whose QK, PV is issued; segments begun
+    uint64_t t_last = globaltimer_ns();
+    while (np < ntiles && ok) {
+      int ready = 0;  // 1: QK(nq), 2: PV(np), 3: waited too long
+      if (lane == 0) {
+        if (nq < ntiles && nq <= np + 1 && mbar_test_wait(smem_u32(&bar_kv[nq & 1]), (nq >> 1) & 1)) {
+          const bool fresh = (meta_s[nq & 3].flags & kFirst) != 0;
+          if (!fresh ||
+              (seg == 0 ? mbar_test_wait(smem_u32(&bar_q0), 0)
+                        : mbar_test_wait(smem_u32(&bar_q), (seg - 1) & 1)))
+            ready = 1;
+        }
+        if (ready == 0 && np < nq && mbar_test_wait(smem_u32(&bar_p[np & 1]), (np >> 1) & 1))
+          ready = 2;
+        if (ready == 0 && (*abort || globaltimer_ns() - t_last > kWaitLimitNs)) ready = 3;
       }
-      m_s[tid] = m;
-      l_s[tid] = l;
-      corr_s[tid] = corr;
+      ready = __shfl_sync(0xffffffffu, ready, 0);
+      if (ready == 1) {
+        tc_fence_after();
+        const int ntok = meta_s[nq & 3].ntok;
+        seg += (meta_s[nq & 3].flags & kFirst) ? 1 : 0;
+        const uint32_t n16 = static_cast<uint32_t>(max(16, (ntok + 15) & ~15));
+        const uint32_t idesc = kIdescF16 | ((n16 >> 3) << 17);
+        const uint32_t kvb = kv_u + (nq & 1) * kTT * 128;
+        const uint32_t d = tmem + (16u << 16) + 256 + 64 * (nq & 1);
+#pragma unroll
+        for (int k = 0; k < kLatent / 16; ++k)
+          umma_bf16_elect(d, sdesc_kmajor_sw128(q_u + (k >> 2) * kRegion + (k & 3) * 32),
+                          sdesc_kmajor_sw128(kvb + (k >> 2) * kKVRegion + (k & 3) * 32), idesc,
+                          k > 0 ? 1u : 0u);
+        umma_commit_elect(&bar_qk[nq & 1]);
+        ++nq;
+        t_last = globaltimer_ns();
+      } else if (ready == 2) {
+        tc_fence_after();
+        const TileMeta m = meta_s[np & 3];
+        const int ks = max(1, (m.ntok + 15) >> 4);
+        const uint32_t kvb = kv_u + (np & 1) * kTT * 128, pb = p_u + (np & 1) * kPBytes;
+#pragma unroll
+        for (int nh = 0; nh < 2; ++nh) {
+#pragma unroll
+          for (int k = 0; k < kTT / 16; ++k)
+            if (k < ks)
+              umma_bf16_elect(tmem + (static_cast<uint32_t>(16 * nh) << 16),
+                              sdesc_kmajor_sw128(pb + k * 32),
+                              sdesc_mn_sw128(kvb + nh * 4 * kKVRegion + k * 16 * 128, kKVRegion, 1024),
+                              kIdescPV, (!(m.flags & kFirst) || k > 0) ? 1u : 0u);
+        }
+        umma_commit_elect(&bar_pv[np & 1]);
+        ++np;
+        t_last = globaltimer_ns();
+      } else if (ready == 3) {
+        ok = false;
+        if (lane == 0) {
+          *abort = 1;
+          atomicExch(&g_device_error, kErrWaitTimeout);
+        }
+      }
     }
-    __syncthreads();
-    for (int h = 0; h < kHeads; ++h) {
-      o[h][0] *= corr_s[h];
-      o[h][1] *= corr_s[h];
-      for (int t = 0; t < kTile; ++t) {
-        o[h][0] += z_s[h][t] * c_s[t * kLatent + 2 * tid];
-        o[h][1] += z_s[h][t] * c_s[t * kLatent + 2 * tid + 1];
+    // every MMA issued here completes before TMEM is released
+    umma_commit_elect(&bar_drain);
+    {
+      volatile int no_abort = 0;
+      if (lane == 0) mbar_wait(&bar_drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else {
+    // ======================= workers ==========================================
+    const int qd = warp & 3, th = warp >> 2, half = lane >> 4;
+    const int m = qd * 16 + (lane & 15);  // this thread's (row, head) pair of the unit
+    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
+    const int hpr = min(p.heads, kM);
+    load_q<kSparse>(p, part.u0, q_u, hs_s[0], warp, kWork / 32, [] {});
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_q0);
+    ok &= mbar_wait(&bar_q0, 0, abort);
+    int seg = -1, row_lim = 0;
+    int64_t out_row = -1;  // row of out of this thread, or -1
+    float hs = 0.f, m_run = -INFINITY, l_run = 0.f;
+#pragma unroll 1
+    for (int t = 0; t < ntiles; ++t) {
+      const int buf = t & 1;
+      ok &= mbar_wait(&bar_kv[buf], (t >> 1) & 1, abort);
+      const TileMeta tm = meta_s[t & 3];
+      if (tm.flags & kFirst) {
+        ++seg;
+        hs = hs_s[seg & 3][m];
+        m_run = -INFINITY;
+        l_run = 0.f;
+        const UnitRows ur = unit_rows<kSparse>(p, tm.unit);
+        const int rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
+        const bool mine = rr < ur.nrows && h < p.heads;
+        out_row = mine ? static_cast<int64_t>(ur.row0 + rr) * p.heads + h : -1;
+        // rows of one unit may see different numbers of tokens
+        row_lim = !kSparse && p.rows_per_unit > 1 ? (mine ? clamp_len(p, ur.row0 + rr) : 0)
+                                                  : 0x7fffffff;
+      }
+      ok &= mbar_wait(&bar_qk[buf], (t >> 1) & 1, abort);
+      tc_fence_after();
+      float z[16];
+      {
+        // lanes 16-31 receive the 32 logits of their head in this warp's half
+        // of the tile; tokens 0-15 of it go to the partner lane
+        uint32_t a[32];
+        tmem_ld_x32_async(tmem + lane_base + 256 + 64 * buf + 32 * th, a);
+        tmem_ld_wait_regs<32>(a);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t v = __shfl_xor_sync(0xffffffffu, a[i], 16);
+          z[i] = __uint_as_float(half ? a[16 + i] : v);
+        }
+      }
+      const float4* te = reinterpret_cast<const float4*>(&te_s[buf][32 * th + 16 * half]);
+      uint32_t tf[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 e = te[i];
+        z[2 * i] = fmaf(z[2 * i] * hs, e.x, e.y);
+        z[2 * i + 1] = fmaf(z[2 * i + 1] * hs, e.z, e.w);
+        tf[2 * i] = __float_as_uint(e.x);
+        tf[2 * i + 1] = __float_as_uint(e.z);
+      }
+      const int lim = min(tm.ntok, row_lim - tm.tile * kTT) - 32 * th - 16 * half;
+      if (__any_sync(0xffffffffu, lim < 16)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = i < lim ? z[i] : -INFINITY;
+      }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mx[i] = fmaxf(fmaxf(z[4 * i], z[4 * i + 1]), fmaxf(z[4 * i + 2], z[4 * i + 3]));
+      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+      if (half == 0) red_m[buf][th][m] = mt;
+      pair_sync(qd);
+      mt = fmaxf(mt, red_m[buf][th ^ 1][m]);
+      float alpha = 1.f;
+      if (m_run == -INFINITY) {
+        m_run = mt;
+      } else if (mt > m_run + kLazy) {
+        alpha = ex2(m_run - mt);
+        m_run = mt;
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at a segment's first tile)
+        ok &= mbar_wait(&bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 128 * th; c < 128 * th + 128; c += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + lane_base + c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= alpha;
+          tmem_st_x32(tmem + lane_base + c, v);
+        }
+      }
+      const float ref = m_run == -INFINITY ? 0.f : m_run - kLift;
+      uint32_t packed[8];
+      float ls[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float e[4];
+        ls[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e[k] = ex2(z[4 * i + k] - ref);
+          ls[i] = fmaf(e[k], __uint_as_float(0x7F000000u - tf[4 * i + k]), ls[i]);  // times 2^-E
+        }
+        packed[2 * i] = h2_bits(__floats2half2_rn(e[0], e[1]));
+        packed[2 * i + 1] = h2_bits(__floats2half2_rn(e[2], e[3]));
+      }
+      float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+      l_run = fmaf(l_run, alpha, lsum);  // this warp's half of the tokens
+      // P buffer t & 1 is free once PV(t-2) is done
+      if (t >= 2) ok &= mbar_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int piece = 4 * th + 2 * half + c;
+        sts128(p_u + buf * kPBytes + m * 128 + ((piece ^ (m & 7)) << 4), packed[4 * c],
+               packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
+      }
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_p[buf]);
+      if (!(tm.flags & kLast)) continue;
+
+      // ---- the segment's output --------------------------------------------
+      if (half == 0) red_l[th][m] = l_run;
+      pair_sync(qd);
+      l_run += red_l[th ^ 1][m];
+      ok &= mbar_wait(&bar_pv[buf], (t >> 1) & 1, abort);
+      tc_fence_after();
+      const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
+      if ((tm.flags & (kHead | kTail)) == (kHead | kTail)) {
+        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+#pragma unroll 1
+        for (int c0 = 128 * th; c0 < 128 * th + 128; c0 += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + lane_base + c0, v);
+          if (out_row >= 0) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kLatent + 256 * half + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 h2 =
+                    __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+                o[k] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        if (p.lse && out_row >= 0 && half == 0 && th == 0)
+          p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
+                                        : -INFINITY;
+      } else {
+        const int slot = 2 * blockIdx.x + ((tm.flags & kHead) ? 1 : 0);
+        float4* dst = p.part_o + static_cast<int64_t>(slot) * (kPartFloats / 4) + tid;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + lane_base + 128 * th + c0, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[(c0 / 4 + i) * kWork] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        if (half == 0 && th == 0) p.part_ml[slot * kM + m] = make_float2(ref_out, l_run);
+      }
+      tc_fence_before();  // O is read before the next segment's first PV
+    }
+  }
+  if (!ok && lane == 0) atomicExch(&g_device_error, kErrWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the units that several CTAs shared: block (c, y) the unit
+// whose first part CTA c left, four dims of every pair for piece y of 32.
+template <bool kSparse>
+__global__ void __launch_bounds__(kWork) k_attn_fp4_combine(const KParams p) {
+  __shared__ float w_s[kMaxGrid][kM];
+  __shared__ float inv_s[kM];
+  pdl_wait();
+  const int c = blockIdx.x, piece = blockIdx.y, tid = threadIdx.x;
+  const int2 cb = p.comb[c];
+  const int parts = cb.y;
+  if (parts == 0) return;
+  auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  // weights 2^(R_i - R) of the parts and 1 / l of each pair: 4 threads a pair
+  {
+    const int m = tid >> 2, j = tid & 3;
+    float R = -INFINITY;
+    for (int i = j; i < parts; i += 4) {
+      const float2 ml = p.part_ml[slot(i) * kM + m];
+      w_s[i][m] = ml.x;
+      R = fmaxf(R, ml.x);
+    }
+    R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, 1));
+    R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, 2));
+    float l = 0.f;
+    for (int i = j; i < parts; i += 4) {
+      const float Ri = w_s[i][m];
+      const float w = Ri == -INFINITY ? (R == -INFINITY ? 1.f : 0.f) : ex2(Ri - R);
+      w_s[i][m] = w;
+      l = fmaf(w, p.part_ml[slot(i) * kM + m].y, l);
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (j == 0) {
+      inv_s[m] = l != 0.f ? 1.f / l : 0.f;
+      if (piece == 0 && p.lse) {
+        const UnitRows ur = unit_rows<kSparse>(p, cb.x);
+        const int hpr = min(p.heads, kM), rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
+        if (rr < ur.nrows && h < p.heads)
+          p.lse[static_cast<int64_t>(ur.row0 + rr) * p.heads + h] =
+              l != 0.f ? (R + log2f(l)) * 0.69314718055994530942f : -INFINITY;
       }
     }
   }
   __syncthreads();
-  for (int h = 0; h < kHeads; ++h) {
-    const float l = l_s[h], inv = l != 0.f ? 1.f / l : 0.f;
-    __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(
-        static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(r) * a.heads + h0 + h) * kLatent);
-    out[tid] = __floats2bfloat162_rn(o[h][0] * inv, o[h][1] * inv);
-    if (tid == 0 && a.lse)
-      a.lse[static_cast<int64_t>(r) * a.heads + h0 + h] = l != 0.f ? m_s[h] + logf(l) : -INFINITY;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int qd = warp & 3, th = warp >> 2, half = lane >> 4, m = qd * 16 + (lane & 15);
+  const UnitRows ur = unit_rows<kSparse>(p, cb.x);
+  const int hpr = min(p.heads, kM), rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
+  if (rr >= ur.nrows || h >= p.heads) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* src = p.part_o + piece * kWork + tid;
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) {
+    const float4 v = src[static_cast<int64_t>(slot(i)) * (kPartFloats / 4)];
+    const float w = w_s[i][m];
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
+  const float inv = inv_s[m];
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(ur.row0 + rr) * p.heads + h) * kLatent +
+                            256 * half + 128 * th + 4 * piece) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+
+template <bool kSparse>
+bool set_attrs() {
+  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && attr_set[dev]) return true;
+  if (cudaFuncSetAttribute(k_attn_fp4<kSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemBytes) != cudaSuccess)
+    return false;
+  if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  return true;
+}
+
+template <bool kSparse>
+cudaError_t launch(const AttnFp4Plan& pl, const KParams& p, cudaStream_t stream) {
+  if (!set_attrs<kSparse>()) return cudaGetLastError();
+  cudaError_t e = launch_ex(k_attn_fp4<kSparse>, dim3(pl.grid), dim3(kThreads), kSmemBytes, stream,
+                            false, 1, p);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  if (pl.ws_bytes > 0) {
+    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, kLatent / 16), dim3(kWork), 0, stream,
+                  true, 1, p);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+  }
+  return cudaGetLastError();
+}
+
+constexpr size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
 AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t max_len,
                           int num_sms) {
-  (void)rows, (void)per_seq, (void)heads, (void)sparse, (void)max_len, (void)num_sms;
-  return AttnFp4Plan{0};
+  AttnFp4Plan pl{};
+  pl.groups = (heads + kM - 1) / kM;
+  pl.rows_per_unit = sparse || heads > kM / 2 ? 1 : kM / heads;
+  if (pl.rows_per_unit > per_seq) pl.rows_per_unit = per_seq;
+  pl.rgs = (per_seq + pl.rows_per_unit - 1) / pl.rows_per_unit;
+  pl.units = rows / per_seq * pl.rgs * pl.groups;
+  int64_t list = max_len;  // tokens in a list, at most
+  if (sparse && list > kTopK * kPool + kPool - 1) list = kTopK * kPool + kPool - 1;
+  int64_t tiles = (list + kTT - 1) / kTT;
+  if (tiles < 1) tiles = 1;
+  const int sms = num_sms < kMaxGrid ? num_sms : kMaxGrid;
+  pl.grid = static_cast<int>(pl.units * tiles < sms ? pl.units * tiles : sms);
+  pl.min_tiles = 1;
+  if (tiles > 1)  // units of one tile are never split
+    pl.ws_bytes = up256(pl.grid * sizeof(int2)) +
+                  static_cast<size_t>(2) * pl.grid * (kM * sizeof(float2) + kPartFloats * 4);
+  return pl;
 }
 
-cudaError_t launch_attn_fp4(const AttnFp4Plan& p, const AttnFp4Args& a, cudaStream_t stream) {
-  (void)p;
-  if (cudaError_t e = cudaFuncSetAttribute(k_attn_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kSmem))
-    return e;
-  k_attn_fp4<<<dim3(a.rows, a.heads / kHeads), kThreads, kSmem, stream>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+cudaError_t launch_attn_fp4(const AttnFp4Plan& pl, const AttnFp4Args& a, cudaStream_t stream) {
+  KParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.codes = a.codes;
+  p.scales = a.scales;
+  p.seq_tok = a.seq_tok;
+  p.len_cap = a.len_cap;
+  p.idx = a.idx;
+  p.count = a.count;
+  p.n_vis = a.n_vis;
+  p.heads = a.heads;
+  p.per_seq = a.per_seq;
+  p.units = pl.units;
+  p.groups = pl.groups;
+  p.rows_per_unit = pl.rows_per_unit;
+  p.rgs = pl.rgs;
+  p.min_tiles = pl.min_tiles;
+  p.scale_log2 = a.sm_scale * 1.44269504088896340736f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  if (pl.ws_bytes > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    p.comb = reinterpret_cast<int2*>(ws);
+    ws += up256(pl.grid * sizeof(int2));
+    p.part_ml = reinterpret_cast<float2*>(ws);
+    ws += static_cast<size_t>(2) * pl.grid * kM * sizeof(float2);
+    p.part_o = reinterpret_cast<float4*>(ws);
+  }
+  return a.idx ? launch<true>(pl, p, stream) : launch<false>(pl, p, stream);
 }
 
 }  // namespace spx

@@ -200,6 +200,9 @@ cudaError_t launch_latent_read_fp4(int B, const uint8_t* codes, const uint8_t* s
                                    int64_t cap_tok, const int64_t* pos, int64_t m,
                                    const int64_t* n_vis, void* out, cudaStream_t stream);
 struct AttnFp4Plan {
+  int units, groups;       // units of 64 (row, head) pairs; groups of 64 heads
+  int rows_per_unit, rgs;  // rows of a unit; units per sequence and head group
+  int grid, min_tiles;     // CTAs; tiles of 64 tokens a CTA takes, at least
   size_t ws_bytes;
 };
 struct AttnFp4Args {
