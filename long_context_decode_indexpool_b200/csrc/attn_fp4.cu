@@ -51,14 +51,18 @@ namespace spx {
 namespace {
 
 constexpr int kWork = 256;       // worker threads (warps 0-7)
-constexpr int kMmaWarp = 8;
-constexpr int kConvWarp0 = 9;
-constexpr int kConvWarps = 7;    // 16 warps in all: 128 registers a thread
-constexpr int kThreads = (kConvWarp0 + kConvWarps) * 32;
+constexpr int kConvWarp0 = 8;    // converter warps 8-15
+constexpr int kConvWarps = 8;
+constexpr int kQkWarp = 16;      // MMA issue
+constexpr int kPvWarp = 17;
+constexpr int kListWarp = 18;    // token positions, L2 prefetch
+constexpr int kThreads = 19 * 32;  // 96 registers a thread
+constexpr int kAhead = 2;        // quarters of a group converted before its buffer is free
+constexpr int kRing = 4;         // tiles the list warp is ahead of a finished one
 constexpr int kTT = 64;          // tokens per tile
 constexpr int kM = 64;           // (row, head) pairs per unit (MMA M)
-constexpr int kOct = 8;          // tokens a converter warp takes at a time
-constexpr int kOcts = kTT / kOct;
+constexpr int kOct = 8;          // tokens of a tile that a converter warp takes
+static_assert(kOct * kConvWarps == kTT, "one group of 8 tokens a warp");
 constexpr int kRegion = 64 * 128;        // [64 rows x 128 B] = 8 KiB
 constexpr int kQBytes = 8 * kRegion;     // 64 KiB
 constexpr int kKVRegion = 2 * kRegion;   // both latent buffers, 64 dims
@@ -94,20 +98,56 @@ struct KParams {
   float4* part_o;  // [2 grid][32 pieces][256 worker threads]
 };
 
-// A tile as its converters describe it to the other roles.
-struct TileMeta {
-  int ntok;   // tokens in its list part (0..64)
+// A tile as the list warp describes it to the other roles.
+struct __align__(16) TileMeta {
   int unit;
-  int tile;   // index in the unit
-  int flags;
+  int tile;  // index in the unit
+  int bits;  // tokens in its part of the list (0..64), and flags
+  int64_t tok0;  // first cache token of its sequence
+  __device__ int ntok() const { return bits & 0xFF; }
 };
-enum : int { kFirst = 1, kLast = 2, kHead = 4, kTail = 8 };  // of the segment; of the unit
+// first, last tile of its segment; the segment has the unit's first, last tile
+enum : int { kFirst = 256, kLast = 512, kHead = 1024, kTail = 2048 };
 
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 __device__ __forceinline__ void pair_sync(int qd) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
+}
+// Waits for a phase with the thread suspended until it completes (or 1 ms has
+// passed: then the limit and the abort flag are looked at, as in mbar_wait).
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(1000000)
+        : "memory");
+    if (done) return true;
+    if (*abort) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicExch(&g_device_error, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+// A warp's wait; the same result for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool r = mbar_sleep(bar, parity, abort);
+  return __all_sync(0xffffffffu, r);
+}
+// Asks `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -122,17 +162,38 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// Shared-memory descriptor of an MN-major operand in the 128-byte-swizzle
-// layout: 64-element groups along MN `lbo` bytes apart, 8-row groups along K
-// `sbo` bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// One tcgen05.mma of fp16 operands by the elected lane (`el`, from elect_lane)
+// of a warp that runs this with all its lanes.  The descriptors come as their
+// low words, which hold the address in 16-byte units, so that a batch of MMAs
+// costs one addition per operand and step.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t el;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(el));
+  return el;
+}
+template <uint32_t kAHi, uint32_t kBHi>
+__device__ __forceinline__ void umma_f16(uint32_t el, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %6};\n\t"
+      "mov.b64 b, {%3, %7};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 e, %0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n\t}" ::"r"(el),
+      "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAHi), "n"(kBHi)
+      : "memory");
+}
+// High descriptor words: 1024 bytes between 8-row groups, version, 128-byte
+// swizzle; low words: the address, and the distance between 64-element groups
+// along MN (in bits 16-29; unused when K-major).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float* v) {
@@ -191,7 +252,7 @@ __device__ __forceinline__ Unit load_unit(const KParams& p, int u) {
   x.n = clamp_len(p, r.row0);
   if (kSparse) {
     const int c = p.count[r.row0];
-    x.cnt = min(min(max(c, 0), kTopK), x.n / kPool);
+    x.cnt = min(min(max(c, 0), kTopK), x.n >> 2);  // 4 tokens a block
     x.S = x.cnt * kPool + (x.n & (kPool - 1));
   } else {
     for (int i = 1; i < r.nrows; ++i) x.n = max(x.n, clamp_len(p, r.row0 + i));
@@ -212,7 +273,7 @@ struct Part {
 
 // Scans the units' tile counts (every thread of the block calls this).
 template <bool kSparse>
-__device__ Part plan_part(const KParams& p, int64_t* scratch /* [20] */) {
+__device__ Part plan_part(const KParams& p, int64_t* scratch /* [kThreads / 32 + 2] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Part part;
   int64_t sum = 0;
@@ -255,13 +316,13 @@ __device__ Part plan_part(const KParams& p, int64_t* scratch /* [20] */) {
     }
     const int64_t off = before + inc - t;
     if (t > 0 && off <= part.begin && part.begin < off + t) {
-      scratch[16] = u;
-      scratch[17] = off;
+      scratch[kThreads / 32] = u;
+      scratch[kThreads / 32 + 1] = off;
     }
     __syncthreads();
     if (part.begin < all) {
-      part.u0 = static_cast<int>(scratch[16]);
-      part.off0 = scratch[17];
+      part.u0 = static_cast<int>(scratch[kThreads / 32]);
+      part.off0 = scratch[kThreads / 32 + 1];
       break;
     }
     base = all;
@@ -336,11 +397,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
                                            ~static_cast<uintptr_t>(1023));
   const uint32_t q_u = smem_u32(sm), kv_u = q_u + kQBytes, p_u = kv_u + kKVBytes;
   __shared__ uint64_t bar_qk[2], bar_pv[2], bar_kv[2], bar_p[2], bar_q0, bar_q, bar_drain;
-  __shared__ TileMeta meta_s[4];
+  __shared__ uint64_t bar_list[kRing], bar_free[kRing];
+  __shared__ TileMeta meta_s[kRing];
+  __shared__ int pos_s[kRing][kTT];  // token positions in the sequence, -1: nothing there
   __shared__ __align__(16) float2 te_s[2][kTT];  // (2^E, E) per token; (1, -inf): nothing there
   __shared__ float hs_s[4][kM];                  // per segment, mod 4
   __shared__ float red_m[2][2][kM], red_l[2][kM];
-  __shared__ int64_t scratch[20];
+  __shared__ int64_t scratch[kThreads / 32 + 2];
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_s;
 
@@ -349,12 +412,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_qk[i], 1);
       mbar_init(&bar_pv[i], 1);
-      mbar_init(&bar_kv[i], kOcts);  // one arrive per group of 8 tokens
+      mbar_init(&bar_kv[i], kConvWarps);
       mbar_init(&bar_p[i], kWork / 32);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar_list[i], 1);
+      mbar_init(&bar_free[i], 1);
     }
     mbar_init(&bar_q0, kWork / 32);
     mbar_init(&bar_q, kConvWarps);
-    mbar_init(&bar_drain, 1);
+    mbar_init(&bar_drain, 2);
     abort_s = 0;
     fence_mbar_init();
   }
@@ -374,90 +441,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 
   if (ntiles == 0) {
     if (tid == 0 && p.comb) p.comb[blockIdx.x] = make_int2(-1, 0);
-  } else if (warp >= kConvWarp0) {
+  } else if (warp >= kConvWarp0 && warp < kQkWarp) {
     // ======================= converter warps ==================================
     const int w = warp - kConvWarp0;
-    const int nx = ntiles * kOcts;
     const int r8 = lane & 7, g4 = lane >> 3;
-    // the unit under the cursor, the one after it, and where they end
-    int u = part.u0, t_end, t_org;  // CTA tiles [t_org, t_end) belong to u (t_org may be < 0)
-    Unit un = load_unit<kSparse>(p, u), nxt{};
-    int64_t off = part.off0;
-    t_org = static_cast<int>(off - part.begin);
-    t_end = t_org + tiles_of(un.S);
-    if (u + 1 < p.units) nxt = load_unit<kSparse>(p, u + 1);
-    int2 comb = make_int2(-1, 0);
-
-    // what is known of a group of 8 tokens before its block id arrives
-    struct Req {
-      int b;       // block id (sparse)
-      int fixed;   // the position where no id decides it; -2: the id does
-      int nblk;
-      int seq;     // sequence of the cache
-      TileMeta m;
-    } rq;
-    struct Oct {
+    struct Oct {  // lane: token r8 of the group, code groups g4, g4 + 4, ..
       uint4 c[4], sc;
       bool valid;
-      TileMeta m;
-    } cur, nx_oct;
-
-    auto request = [&](int x) {  // group x of the CTA; x grows by less than a tile
-      const int t = x >> 3;
-      while (t >= t_end) {  // next unit
-        ++u;
-        un = nxt;
-        t_org = t_end;
-        t_end = t_org + tiles_of(un.S);
-        if (u + 1 < p.units) nxt = load_unit<kSparse>(p, u + 1);
-      }
-      const int tile = t - t_org;
-      const int last = min(t_end, ntiles) - 1;
-      rq.m.unit = u;
-      rq.m.tile = tile;
-      rq.m.ntok = max(0, min(un.S - tile * kTT, kTT));
-      rq.m.flags = ((t == max(t_org, 0)) ? kFirst : 0) | (t == last ? kLast : 0) |
-                   (t_org >= 0 ? kHead : 0) | (t_end <= ntiles ? kTail : 0);
-      if (t_org >= 0 && t_end > ntiles) {  // the split unit that begins here
-        const int64_t last_tile = part.begin + t_end - 1;
-        comb = make_int2(u, static_cast<int>(last_tile / part.quota) -
-                                static_cast<int>(blockIdx.x) + 1);
-      }
-      const int j = tile * kTT + (x & 7) * kOct + r8;
-      const UnitRows ur = unit_rows<kSparse>(p, u);
-      rq.seq = kSparse ? ur.row0 : ur.row0 / p.per_seq;
-      rq.fixed = j < un.S ? j : -1;
-      rq.b = -1;
-      rq.nblk = un.n / kPool;
-      if (kSparse && rq.fixed >= 0) {
-        if (j < un.cnt * kPool) {
-          rq.fixed = -2;
-          rq.b = p.idx[static_cast<int64_t>(ur.row0) * kTopK + (j >> 2)];
-        } else {
-          rq.fixed = rq.nblk * kPool + (j - un.cnt * kPool);
-        }
-      }
-    };
-    auto load = [&](Oct& o) {  // the codes and scales of the requested group
-      int pos = rq.fixed;
-      if (kSparse && pos == -2) pos = rq.b < 0 || rq.b >= rq.nblk ? -1 : rq.b * kPool + (r8 & 3);
-      o.m = rq.m;
-      o.valid = pos >= 0;
-      o.sc = make_uint4(0u, 0u, 0u, 0u);
+      int bits;
+    } raw;
+    auto load = [&](int t) {  // the codes and scales of tile t's group
+      ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
+      const int pos = ok ? pos_s[t % kRing][w * kOct + r8] : -1;
+      raw.bits = meta_s[t % kRing].bits;
+      raw.valid = pos >= 0;
+      raw.sc = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o.c[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (o.valid) {
-        const int64_t at = static_cast<int64_t>(rq.seq) * p.seq_tok + pos;
-        o.sc = *reinterpret_cast<const uint4*>(p.scales + at * kFp4Groups);
+      for (int k = 0; k < 4; ++k) raw.c[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (raw.valid) {
+        const int64_t at = meta_s[t % kRing].tok0 + pos;
+        raw.sc = *reinterpret_cast<const uint4*>(p.scales + at * kFp4Groups);
         const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * kFp4CodeBytes);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o.c[k] = src[4 * k + g4];
+        for (int k = 0; k < 4; ++k) raw.c[k] = src[4 * k + g4];
       }
     };
-    auto convert = [&](const Oct& o, int x) {
-      const int t = x >> 3, oct = x & 7, buf = t & 1;
-      if (t >= 2) ok &= mbar_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
-      if (oct == 0 && lane == 0) meta_s[t & 3] = o.m;
+    int seg = 0;  // segments begun before this one
+    auto step = [&](const Oct& o, int t) {
+      const int buf = t & 1;
+      if ((o.bits & kFirst) && t > 0) {
+        // a later segment begins: this warp's share of the new queries, once
+        // the last product with the old ones is done (and before its arrival
+        // for the tile, which publishes hs_s to the workers)
+        ++seg;
+        load_q<kSparse>(p, meta_s[t % kRing].unit, q_u, hs_s[seg & 3], w, kConvWarps, [&] {
+          ok &= warp_wait(&bar_qk[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
+        });
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q);
+      }
       // the row's largest exponent byte but 255 (a NaN group): bytes + 1 mod
       // 256, a word of four per lane
       const uint32_t sw[4] = {o.sc.x, o.sc.y, o.sc.z, o.sc.w};
@@ -468,137 +491,214 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       // biased exponent of the row, kept where 2^E and 2^-E are normal
       const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
-      const int row = oct * kOct + r8;
+      __half2 s2[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int b = static_cast<int>((sw[k] >> (8 * g4)) & 0xFFu);
+        // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group)
+        __half s = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
+        if (b == kFp4NanByte) s = __ushort_as_half(0x7E00);
+        s2[k] = __half2half2(s);
+      }
+      const int row = w * kOct + r8;
+      const uint32_t base = kv_u + (buf * kTT + row) * 128;
+      uint32_t v[16 * kAhead];
+      auto to_half = [&](int k, uint32_t* dst) {
+        const uint32_t in[4] = {o.c[k].x, o.c[k].y, o.c[k].z, o.c[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[4];
+          fp4x8_to_half2x4(in[i], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[4 * i + e] = h2_bits(__hmul2(*reinterpret_cast<__half2*>(&h[e]), s2[k]));
+        }
+      };
+      auto put = [&](int k, const uint32_t* src) {
+        const int g = 4 * k + g4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sts128(base + (g >> 1) * kKVRegion + (((4 * (g & 1) + i) ^ r8) << 4), src[4 * i],
+                 src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) to_half(k, v + 16 * k);
+      if (t >= 2) ok &= warp_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
       if (lane < kOct)
         te_s[buf][row] = o.valid ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
                                  : make_float2(1.f, -INFINITY);
       // tokens up to the next multiple of 16 take part in the products
-      if (oct * kOct < max(16, (o.m.ntok + 15) & ~15)) {
-        const uint32_t base = kv_u + (buf * kTT + row) * 128;
+      if (w * kOct < max(16, ((o.bits & 0xFF) + 15) & ~15)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int g = 4 * k + g4;
-          const int b = static_cast<int>((sw[k] >> (8 * g4)) & 0xFFu);
-          // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group)
-          __half s = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
-          if (b == kFp4NanByte) s = __ushort_as_half(0x7E00);
-          const __half2 s2 = __half2half2(s);
-          const uint32_t in[4] = {o.c[k].x, o.c[k].y, o.c[k].z, o.c[k].w};
+        for (int k = 0; k < kAhead; ++k) put(k, v + 16 * k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = h2_bits(__hmul2(fp4x2_to_half2(in[i] >> (8 * e)), s2));
-            sts128(base + (g >> 1) * kKVRegion + (((4 * (g & 1) + i) ^ r8) << 4), v[0], v[1], v[2],
-                   v[3]);
-          }
+        for (int k = kAhead; k < 4; ++k) {
+          uint32_t h[16];
+          to_half(k, h);
+          put(k, h);
         }
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_kv[buf]);
     };
-
-    int seg = 0, seg_tile = 0;  // segments begun, first tile of the current one
-    request(w);
-    load(cur);
-    if (w + kConvWarps < nx) request(w + kConvWarps);
+    // A group's registers are copied (which waits for its loads) before the
+    // next group's loads are issued: with two sets in turn the wait for the
+    // older loads also waited for the newer ones, 1,300 cycles a group.
+    // A group's registers are copied (which waits for its loads) before the
+    // next group's loads are issued: with two sets in turn the wait for the
+    // older loads also waited for the newer ones, 1,300 cycles a group.
+    load(0);
 #pragma unroll 1
-    for (int x = w; x < nx; x += kConvWarps) {
-      if (x + kConvWarps < nx) {
-        load(nx_oct);
-        if (x + 2 * kConvWarps < nx) request(x + 2 * kConvWarps);
-      }
-      const int t = x >> 3;
-      if ((cur.m.flags & kFirst) && t > seg_tile) {
-        // this warp's first group of a later segment: its share of the new
-        // queries, once the last product with the old ones is done (and
-        // before its arrival for the tile, which publishes hs_s to the
-        // workers)
-        seg_tile = t;
-        ++seg;
-        load_q<kSparse>(p, cur.m.unit, q_u, hs_s[seg & 3], w, kConvWarps, [&] {
-          ok &= mbar_wait(&bar_qk[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
-        });
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_q);
-      }
-      convert(cur, x);
-      cur = nx_oct;
+    for (int t = 0; t < ntiles; ++t) {
+      const Oct cur = raw;
+      if (t + 1 < ntiles) load(t + 1);
+      step(cur, t);
     }
-    if (w == 0 && lane == 0 && p.comb) p.comb[blockIdx.x] = comb;
-  } else if (warp == kMmaWarp) {
-    // ======================= MMA issuer =======================================
-    // The whole warp runs the loop (lane 0 polls the barriers and broadcasts
-    // the decision), so the descriptors are warp-uniform.
-    int nq = 0, np = 0, seg = 0;  // tiles whose QK, PV is issued; segments begun
-    uint64_t t_last = globaltimer_ns();
-    while (np < ntiles && ok) {
-      int ready = 0;  // 1: QK(nq), 2: PV(np), 3: waited too long
-      if (lane == 0) {
-        if (nq < ntiles && nq <= np + 1 && mbar_test_wait(smem_u32(&bar_kv[nq & 1]), (nq >> 1) & 1)) {
-          const bool fresh = (meta_s[nq & 3].flags & kFirst) != 0;
-          if (!fresh ||
-              (seg == 0 ? mbar_test_wait(smem_u32(&bar_q0), 0)
-                        : mbar_test_wait(smem_u32(&bar_q), (seg - 1) & 1)))
-            ready = 1;
+  } else if (warp == kQkWarp || warp == kPvWarp) {
+    // ======================= MMA issue ========================================
+    // One warp issues S = Q C^T, the other O += P C.  A whole warp runs its
+    // loop and one elected lane issues, so the descriptors are warp-uniform.
+    const uint32_t el = elect_lane();
+    const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+    if (warp == kQkWarp) {
+      const uint32_t q_lo = desc_lo(q_u, 16);
+      int seg = 0;  // segments begun
+#pragma unroll 1
+      for (int t = 0; t < ntiles && ok; ++t) {
+        // S buffer t & 1 is free once the softmax of tile t-2 has read it
+        if (t >= 2) ok &= warp_wait(&bar_p[t & 1], ((t - 2) >> 1) & 1, abort);
+        ok &= warp_wait(&bar_kv[t & 1], (t >> 1) & 1, abort);
+        const int bits = meta_s[t % kRing].bits;
+        if (bits & kFirst) {
+          ok &= seg == 0 ? warp_wait(&bar_q0, 0, abort) : warp_wait(&bar_q, (seg - 1) & 1, abort);
+          ++seg;
         }
-        if (ready == 0 && np < nq && mbar_test_wait(smem_u32(&bar_p[np & 1]), (np >> 1) & 1))
-          ready = 2;
-        if (ready == 0 && (*abort || globaltimer_ns() - t_last > kWaitLimitNs)) ready = 3;
-      }
-      ready = __shfl_sync(0xffffffffu, ready, 0);
-      if (ready == 1) {
+        if (!ok) break;  // uniform
         tc_fence_after();
-        const int ntok = meta_s[nq & 3].ntok;
-        seg += (meta_s[nq & 3].flags & kFirst) ? 1 : 0;
-        const uint32_t n16 = static_cast<uint32_t>(max(16, (ntok + 15) & ~15));
+        const uint32_t n16 = static_cast<uint32_t>(max(16, ((bits & 0xFF) + 15) & ~15));
         const uint32_t idesc = kIdescF16 | ((n16 >> 3) << 17);
-        const uint32_t kvb = kv_u + (nq & 1) * kTT * 128;
-        const uint32_t d = tmem + (16u << 16) + 256 + 64 * (nq & 1);
+        const uint32_t d = tm0 + (16u << 16) + 256 + 64 * (t & 1);
+        const uint32_t k_lo = desc_lo(kv_u + (t & 1) * kTT * 128, 16);
 #pragma unroll
         for (int k = 0; k < kLatent / 16; ++k)
-          umma_bf16_elect(d, sdesc_kmajor_sw128(q_u + (k >> 2) * kRegion + (k & 3) * 32),
-                          sdesc_kmajor_sw128(kvb + (k >> 2) * kKVRegion + (k & 3) * 32), idesc,
-                          k > 0 ? 1u : 0u);
-        umma_commit_elect(&bar_qk[nq & 1]);
-        ++nq;
-        t_last = globaltimer_ns();
-      } else if (ready == 2) {
+          umma_f16<kDescHi, kDescHi>(el, d, q_lo + (((k >> 2) * kRegion + (k & 3) * 32) >> 4),
+                                     k_lo + (((k >> 2) * kKVRegion + (k & 3) * 32) >> 4), idesc,
+                                     k > 0 ? 1u : 0u);
+        umma_commit_elect(&bar_qk[t & 1]);
+      }
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < ntiles && ok; ++t) {
+        ok &= warp_wait(&bar_kv[t & 1], (t >> 1) & 1, abort);
+        const int bits = meta_s[t % kRing].bits;
+        const int ks = max(1, ((bits & 0xFF) + 15) >> 4);
+        ok &= warp_wait(&bar_p[t & 1], (t >> 1) & 1, abort);
+        if (!ok) break;  // uniform
         tc_fence_after();
-        const TileMeta m = meta_s[np & 3];
-        const int ks = max(1, (m.ntok + 15) >> 4);
-        const uint32_t kvb = kv_u + (np & 1) * kTT * 128, pb = p_u + (np & 1) * kPBytes;
+        const uint32_t p_lo = desc_lo(p_u + (t & 1) * kPBytes, 16);
+        const uint32_t c_lo = desc_lo(kv_u + (t & 1) * kTT * 128, kKVRegion);
 #pragma unroll
         for (int nh = 0; nh < 2; ++nh) {
 #pragma unroll
           for (int k = 0; k < kTT / 16; ++k)
             if (k < ks)
-              umma_bf16_elect(tmem + (static_cast<uint32_t>(16 * nh) << 16),
-                              sdesc_kmajor_sw128(pb + k * 32),
-                              sdesc_mn_sw128(kvb + nh * 4 * kKVRegion + k * 16 * 128, kKVRegion, 1024),
-                              kIdescPV, (!(m.flags & kFirst) || k > 0) ? 1u : 0u);
+              umma_f16<kDescHi, kDescHi>(el, tm0 + (static_cast<uint32_t>(16 * nh) << 16),
+                                         p_lo + (k * 32 >> 4),
+                                         c_lo + ((nh * 4 * kKVRegion + k * 16 * 128) >> 4), kIdescPV,
+                                         (!(bits & kFirst) || k > 0) ? 1u : 0u);
         }
-        umma_commit_elect(&bar_pv[np & 1]);
-        ++np;
-        t_last = globaltimer_ns();
-      } else if (ready == 3) {
-        ok = false;
-        if (lane == 0) {
-          *abort = 1;
-          atomicExch(&g_device_error, kErrWaitTimeout);
-        }
+        umma_commit_elect(&bar_pv[t & 1]);
+        umma_commit_elect(&bar_free[t % kRing]);
       }
     }
-    // every MMA issued here completes before TMEM is released
+    // every MMA issued completes before TMEM is released
     umma_commit_elect(&bar_drain);
     {
       volatile int no_abort = 0;
-      if (lane == 0) mbar_wait(&bar_drain, 0, &no_abort);
+      warp_wait(&bar_drain, 0, &no_abort);
     }
-    __syncwarp();
-  } else {
+  } else if (warp == kListWarp) {
+    // ======================= list warp ========================================
+    // The token positions of tile after tile (two tokens a lane), block ids
+    // loaded one tile ahead; the rows are asked into L2 here.
+    int u = part.u0;
+    Unit un = load_unit<kSparse>(p, u), nxt{};
+    int t_org = static_cast<int>(part.off0 - part.begin);  // CTA tiles [t_org, t_end) are u's
+    int t_end = t_org + tiles_of(un.S);
+    int2 comb = make_int2(-1, 0);
+    int64_t tok0;
+    const int32_t* ids;
+    auto enter_unit = [&] {
+      if (u + 1 < p.units) nxt = load_unit<kSparse>(p, u + 1);
+      const int row0 = unit_rows<kSparse>(p, u).row0;
+      tok0 = static_cast<int64_t>(kSparse ? row0 : row0 / p.per_seq) * p.seq_tok;
+      ids = p.idx + static_cast<int64_t>(row0) * kTopK;  // (unused when dense)
+      if (t_org >= 0 && t_end > ntiles)  // the split unit that begins here
+        comb = make_int2(u, static_cast<int>((part.begin + t_end - 1) / part.quota) -
+                                static_cast<int>(blockIdx.x) + 1);
+    };
+    enter_unit();
+    int b[2], fixed[2], nblk = 0;  // of the next tile: ids, or positions no id decides (-2: it does)
+    TileMeta m;
+    auto request = [&](int t) {
+      if (t >= t_end) {
+        ++u;
+        un = nxt;
+        t_org = t_end;
+        t_end = t_org + tiles_of(un.S);
+        enter_unit();
+      }
+      m.unit = u;
+      m.tile = t - t_org;
+      m.tok0 = tok0;
+      m.bits = max(0, min(un.S - m.tile * kTT, kTT)) | (t == max(t_org, 0) ? kFirst : 0) |
+               (t == min(t_end, ntiles) - 1 ? kLast : 0) | (t_org >= 0 ? kHead : 0) |
+               (t_end <= ntiles ? kTail : 0);
+      nblk = un.n >> 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = m.tile * kTT + 32 * i + lane;
+        fixed[i] = j < un.S ? j : -1;
+        b[i] = -1;
+        if (kSparse && fixed[i] >= 0) {
+          if (j < un.cnt * kPool) {
+            fixed[i] = -2;
+            b[i] = ids[j >> 2];
+          } else {
+            fixed[i] = nblk * kPool + (j - un.cnt * kPool);
+          }
+        }
+      }
+    };
+    request(0);
+#pragma unroll 1
+    for (int t = 0; t < ntiles && ok; ++t) {
+      const int slot = t % kRing;
+      if (t >= kRing) ok &= warp_wait(&bar_free[slot], (t / kRing - 1) & 1, abort);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int pos = fixed[i];
+        if (kSparse && pos == -2) pos = b[i] < 0 || b[i] >= nblk ? -1 : b[i] * kPool + (lane & 3);
+        pos_s[slot][32 * i + lane] = pos;
+        if (kSparse && (lane & 3) == 0 && pos >= 0) {  // a block (or the partial tail's tokens)
+          const uint32_t rows = static_cast<uint32_t>(min(kPool, (m.bits & 0xFF) - 32 * i - lane));
+          l2_prefetch(p.codes + (m.tok0 + pos) * kFp4CodeBytes, rows * kFp4CodeBytes);
+          l2_prefetch(p.scales + (m.tok0 + pos) * kFp4Groups, rows * kFp4Groups);
+        }
+      }
+      if (!kSparse && lane == 0 && (m.bits & 0xFF) > 0) {
+        const uint32_t rows = static_cast<uint32_t>(m.bits & 0xFF);
+        l2_prefetch(p.codes + (m.tok0 + m.tile * kTT) * kFp4CodeBytes, rows * kFp4CodeBytes);
+        l2_prefetch(p.scales + (m.tok0 + m.tile * kTT) * kFp4Groups, rows * kFp4Groups);
+      }
+      if (lane == 0) meta_s[slot] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_list[slot]);
+      if (t + 1 < ntiles) request(t + 1);
+    }
+    if (lane == 0 && p.comb) p.comb[blockIdx.x] = comb;
+  } else if (warp < kConvWarp0) {
     // ======================= workers ==========================================
     const int qd = warp & 3, th = warp >> 2, half = lane >> 4;
     const int m = qd * 16 + (lane & 15);  // this thread's (row, head) pair of the unit
@@ -608,16 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar_q0);
-    ok &= mbar_wait(&bar_q0, 0, abort);
+    ok &= warp_wait(&bar_q0, 0, abort);
     int seg = -1, row_lim = 0;
     int64_t out_row = -1;  // row of out of this thread, or -1
     float hs = 0.f, m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1
     for (int t = 0; t < ntiles; ++t) {
       const int buf = t & 1;
-      ok &= mbar_wait(&bar_kv[buf], (t >> 1) & 1, abort);
-      const TileMeta tm = meta_s[t & 3];
-      if (tm.flags & kFirst) {
+      ok &= warp_wait(&bar_kv[buf], (t >> 1) & 1, abort);
+      const TileMeta tm = meta_s[t % kRing];
+      if (tm.bits & kFirst) {
         ++seg;
         hs = hs_s[seg & 3][m];
         m_run = -INFINITY;
@@ -630,7 +730,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         row_lim = !kSparse && p.rows_per_unit > 1 ? (mine ? clamp_len(p, ur.row0 + rr) : 0)
                                                   : 0x7fffffff;
       }
-      ok &= mbar_wait(&bar_qk[buf], (t >> 1) & 1, abort);
+      const float4* te = reinterpret_cast<const float4*>(&te_s[buf][32 * th + 16 * half]);
+      float4 e2[8];  // (2^E, E) of this thread's 16 tokens
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e2[i] = te[i];
+      ok &= warp_wait(&bar_qk[buf], (t >> 1) & 1, abort);
       tc_fence_after();
       float z[16];
       {
@@ -645,17 +749,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           z[i] = __uint_as_float(half ? a[16 + i] : v);
         }
       }
-      const float4* te = reinterpret_cast<const float4*>(&te_s[buf][32 * th + 16 * half]);
       uint32_t tf[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 e = te[i];
+        const float4 e = e2[i];
         z[2 * i] = fmaf(z[2 * i] * hs, e.x, e.y);
         z[2 * i + 1] = fmaf(z[2 * i + 1] * hs, e.z, e.w);
         tf[2 * i] = __float_as_uint(e.x);
         tf[2 * i + 1] = __float_as_uint(e.z);
       }
-      const int lim = min(tm.ntok, row_lim - tm.tile * kTT) - 32 * th - 16 * half;
+      const int lim = min(tm.ntok(), row_lim - tm.tile * kTT) - 32 * th - 16 * half;
       if (__any_sync(0xffffffffu, lim < 16)) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) z[i] = i < lim ? z[i] : -INFINITY;
@@ -667,47 +770,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
       if (half == 0) red_m[buf][th][m] = mt;
+      // The weights, against the running maximum as it stands: most tiles leave
+      // it, so the exchange with the other warp of the pair ends behind them.
+      uint32_t packed[8];
+      float ls[4], alpha = 1.f;
+      auto weights = [&] {
+        const float ref = m_run == -INFINITY ? 0.f : m_run - kLift;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float e[4];
+          ls[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e[k] = ex2(z[4 * i + k] - ref);
+            ls[i] = fmaf(e[k], __uint_as_float(0x7F000000u - tf[4 * i + k]), ls[i]);  // times 2^-E
+          }
+          packed[2 * i] = h2_bits(__floats2half2_rn(e[0], e[1]));
+          packed[2 * i + 1] = h2_bits(__floats2half2_rn(e[2], e[3]));
+        }
+      };
+      weights();
       pair_sync(qd);
       mt = fmaxf(mt, red_m[buf][th ^ 1][m]);
-      float alpha = 1.f;
-      if (m_run == -INFINITY) {
-        m_run = mt;
-      } else if (mt > m_run + kLazy) {
-        alpha = ex2(m_run - mt);
-        m_run = mt;
-      }
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at a segment's first tile)
-        ok &= mbar_wait(&bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
-        tc_fence_after();
+      const bool raise = mt > m_run + kLazy || (m_run == -INFINITY && mt > m_run);
+      if (__any_sync(0xffffffffu, raise)) {
+        // (the same decision in both warps of the pair)
+        if (raise) {
+          if (m_run != -INFINITY) alpha = ex2(m_run - mt);
+          m_run = mt;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at a segment's first tile)
+          ok &= warp_wait(&bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = 128 * th; c < 128 * th + 128; c += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(tmem + lane_base + c, v);
+          for (int c = 128 * th; c < 128 * th + 128; c += 32) {
+            float v[32];
+            tmem_ld_32x32b_x32(tmem + lane_base + c, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= alpha;
-          tmem_st_x32(tmem + lane_base + c, v);
+            for (int i = 0; i < 32; ++i) v[i] *= alpha;
+            tmem_st_x32(tmem + lane_base + c, v);
+          }
         }
-      }
-      const float ref = m_run == -INFINITY ? 0.f : m_run - kLift;
-      uint32_t packed[8];
-      float ls[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float e[4];
-        ls[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          e[k] = ex2(z[4 * i + k] - ref);
-          ls[i] = fmaf(e[k], __uint_as_float(0x7F000000u - tf[4 * i + k]), ls[i]);  // times 2^-E
-        }
-        packed[2 * i] = h2_bits(__floats2half2_rn(e[0], e[1]));
-        packed[2 * i + 1] = h2_bits(__floats2half2_rn(e[2], e[3]));
+        weights();
       }
       float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
       lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
       l_run = fmaf(l_run, alpha, lsum);  // this warp's half of the tokens
-      // P buffer t & 1 is free once PV(t-2) is done
-      if (t >= 2) ok &= mbar_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
+      // P buffer t & 1 is free: the converters refilled latent buffer t & 1,
+      // so PV(t-2) is done
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int piece = 4 * th + 2 * half + c;
@@ -718,16 +828,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_p[buf]);
-      if (!(tm.flags & kLast)) continue;
+      if (!(tm.bits & kLast)) continue;
 
       // ---- the segment's output --------------------------------------------
       if (half == 0) red_l[th][m] = l_run;
       pair_sync(qd);
       l_run += red_l[th ^ 1][m];
-      ok &= mbar_wait(&bar_pv[buf], (t >> 1) & 1, abort);
+      ok &= warp_wait(&bar_pv[buf], (t >> 1) & 1, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
-      if ((tm.flags & (kHead | kTail)) == (kHead | kTail)) {
+      if ((tm.bits & (kHead | kTail)) == (kHead | kTail)) {
         const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
 #pragma unroll 1
         for (int c0 = 128 * th; c0 < 128 * th + 128; c0 += 32) {
@@ -752,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
                                         : -INFINITY;
       } else {
-        const int slot = 2 * blockIdx.x + ((tm.flags & kHead) ? 1 : 0);
+        const int slot = 2 * blockIdx.x + ((tm.bits & kHead) ? 1 : 0);
         float4* dst = p.part_o + static_cast<int64_t>(slot) * (kPartFloats / 4) + tid;
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {

@@ -42,4 +42,16 @@ __device__ __forceinline__ __half2 fp4x2_to_half2(uint32_t byte) {
   return *reinterpret_cast<const __half2*>(&h);
 }
 
+// The eight values of four code bytes, two to a register.
+__device__ __forceinline__ void fp4x8_to_half2x4(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+}
+
 }  // namespace spx
