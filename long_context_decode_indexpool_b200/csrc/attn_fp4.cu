@@ -57,18 +57,19 @@ constexpr int kQkWarp = 16;      // MMA issue
 constexpr int kPvWarp = 17;
 constexpr int kListWarp = 18;    // token positions, L2 prefetch
 constexpr int kThreads = 19 * 32;  // 96 registers a thread
-constexpr int kAhead = 2;        // quarters of a group converted before its buffer is free
-constexpr int kRing = 4;         // tiles the list warp is ahead of a finished one
+constexpr int kRing = 8;         // tiles the list warp is ahead of a finished one
 constexpr int kTT = 64;          // tokens per tile
 constexpr int kM = 64;           // (row, head) pairs per unit (MMA M)
 constexpr int kOct = 8;          // tokens of a tile that a converter warp takes
 static_assert(kOct * kConvWarps == kTT, "one group of 8 tokens a warp");
-constexpr int kRegion = 64 * 128;        // [64 rows x 128 B] = 8 KiB
-constexpr int kQBytes = 8 * kRegion;     // 64 KiB
-constexpr int kKVRegion = 2 * kRegion;   // both latent buffers, 64 dims
-constexpr int kKVBytes = 8 * kKVRegion;  // 128 KiB
-constexpr int kPBytes = kRegion;         // [64 x 64 tokens] fp16, two buffers
-constexpr int kSmemBytes = 1024 + kQBytes + kKVBytes + 2 * kPBytes;
+constexpr int kRegion = 64 * 128;         // [64 rows x 128 B] = 8 KiB
+constexpr int kSlotBytes = 8 * kRegion;   // a tile (or the queries) in fp16: 64 KiB
+constexpr int kSlots = 3;
+constexpr int kPBytes = kRegion;          // [64 x 64 tokens] fp16, two buffers
+constexpr int kSmemBytes = 1024 + kSlots * kSlotBytes + 2 * kPBytes;
+// TMEM columns: in lanes 0-15 of each quarter the queries (two fp16 values a
+// column) and the logits, in lanes 16-31 the output
+constexpr int kColS = 256;
 constexpr float kLazy = 8.f;   // the maximum is raised when exceeded by more
 constexpr float kLift = 7.f;   // P = 2^(z - max + 7)
 constexpr int kMaxGrid = 160;  // CTAs (one per SM, at most)
@@ -95,7 +96,7 @@ struct KParams {
   float* lse;
   int2* comb;      // [grid] (unit, CTAs it spans) of the split unit that begins in a CTA
   float2* part_ml; // [2 grid][64] (R, l)
-  float4* part_o;  // [2 grid][32 pieces][256 worker threads]
+  float4* part_o;  // [2 grid][64 pieces of 4 dims][8 worker warps][16 pairs]
 };
 
 // A tile as the list warp describes it to the other roles.
@@ -175,17 +176,32 @@ __device__ __forceinline__ uint32_t elect_lane() {
       : "=r"(el));
   return el;
 }
-template <uint32_t kAHi, uint32_t kBHi>
+template <uint32_t kHi>
 __device__ __forceinline__ void umma_f16(uint32_t el, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%2, %6};\n\t"
-      "mov.b64 b, {%3, %7};\n\t"
+      "mov.b64 b, {%3, %6};\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
       "setp.ne.b32 e, %0, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n\t}" ::"r"(el),
-      "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kAHi), "n"(kBHi)
+      "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kHi)
+      : "memory");
+}
+// The same with A in TMEM (M = 64: lanes 0-15 of each quarter, as D's at lane
+// offset 0; eight columns per step of K = 16).  A at lane offset 16 is a
+// misaligned address.
+template <uint32_t kHi>
+__device__ __forceinline__ void umma_f16_ta(uint32_t el, uint32_t d_tmem, uint32_t a_tmem,
+                                            uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%3, %6};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 e, %0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n\t}" ::"r"(el),
+      "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kHi)
       : "memory");
 }
 // High descriptor words: 1024 bytes between 8-row groups, version, 128-byte
@@ -196,22 +212,16 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float* v) {
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
       "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
-      "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
-      "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-      "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
-      "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
-      "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -332,12 +342,13 @@ __device__ Part plan_part(const KParams& p, int64_t* scratch /* [kThreads / 32 +
 }
 
 // ---- queries ------------------------------------------------------------------
-// Rows w, w + nw, .. of the unit's 64 query rows to shared memory as fp16,
-// each scaled by a power of two; hs[m] is what a product with it is multiplied
-// by.  `wait` is called between the first loads and the first store.
+// Rows w, w + 8, .. of the unit's 64 query rows to a shared-memory slot as
+// fp16, each scaled by a power of two; hs[m] is what a product with it is
+// multiplied by.  `wait` is called between the first loads and the first store.
 template <bool kSparse, typename Wait>
-__device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t q_u, float* hs, int w,
-                                       int nw, Wait wait) {
+__device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t slot, float* hs, int w,
+                                       Wait wait) {
+  constexpr int nw = kConvWarps;
   const int lane = threadIdx.x & 31;
   const UnitRows r = unit_rows<kSparse>(p, u);
   const int hpr = min(p.heads, kM);  // heads of a row in the unit
@@ -350,7 +361,7 @@ __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t q_u, fl
       const int m = m0 + i * nw;
       const int rr = m / hpr, h = r.hg * kM + m - rr * hpr;
       v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (m < kM && rr < r.nrows && h < p.heads) {
+      if (rr < r.nrows && h < p.heads) {
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (static_cast<int64_t>(r.row0 + rr) * p.heads + h) * kLatent);
         v[i][0] = src[lane];
@@ -362,7 +373,6 @@ __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t q_u, fl
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = m0 + i * nw;
-      if (m >= kM) break;  // uniform
       const uint32_t mask = 0x7FFF7FFFu;
       uint32_t a = __vmaxu2(__vmaxu2(v[i][0].x & mask, v[i][0].y & mask),
                             __vmaxu2(v[i][0].z & mask, v[i][0].w & mask));
@@ -381,7 +391,7 @@ __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t q_u, fl
           o[k] = h2_bits(__floats2half2_rn(__uint_as_float(in[k] << 16) * f,
                                            __uint_as_float(in[k] & 0xFFFF0000u) * f));
         const int piece = 32 * half + lane;
-        sts128(q_u + (piece >> 3) * kRegion + m * 128 + (((piece & 7) ^ (m & 7)) << 4), o[0], o[1],
+        sts128(slot + (piece >> 3) * kRegion + m * 128 + (((piece & 7) ^ (m & 7)) << 4), o[0], o[1],
                o[2], o[3]);
       }
       if (lane == 0) hs[m] = p.scale_log2 * __int_as_float((127 - s) << 23);
@@ -393,15 +403,15 @@ __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t q_u, fl
 template <bool kSparse>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   extern __shared__ uint8_t dyn[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
-  const uint32_t q_u = smem_u32(sm), kv_u = q_u + kQBytes, p_u = kv_u + kKVBytes;
-  __shared__ uint64_t bar_qk[2], bar_pv[2], bar_kv[2], bar_p[2], bar_q0, bar_q, bar_drain;
-  __shared__ uint64_t bar_list[kRing], bar_free[kRing];
+  const uint32_t slot_u = (smem_u32(dyn) + 1023) & ~1023u, p_u = slot_u + kSlots * kSlotBytes;
+  __shared__ uint64_t bar_full[kSlots], bar_free[kSlots];  // slots: filled, given back
+  __shared__ uint64_t bar_list[kRing], bar_used[kRing];    // list ring: filled, tile done
+  __shared__ uint64_t bar_qk[2], bar_p[2], bar_pv[2];      // S(t), P(t), O of tile t & 1 ready
+  __shared__ uint64_t bar_q, bar_drain;                    // queries in TMEM; all MMAs done
   __shared__ TileMeta meta_s[kRing];
   __shared__ int pos_s[kRing][kTT];  // token positions in the sequence, -1: nothing there
-  __shared__ __align__(16) float2 te_s[2][kTT];  // (2^E, E) per token; (1, -inf): nothing there
-  __shared__ float hs_s[4][kM];                  // per segment, mod 4
+  __shared__ __align__(16) float2 te_s[kSlots][kTT];  // (2^E, E) per token; (1, -inf): nothing there
+  __shared__ float hs_s[4][kM];                       // per segment, mod 4
   __shared__ float red_m[2][2][kM], red_l[2][kM];
   __shared__ int64_t scratch[kThreads / 32 + 2];
   __shared__ uint32_t tmem_holder;
@@ -409,18 +419,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_qk[i], 1);
-      mbar_init(&bar_pv[i], 1);
-      mbar_init(&bar_kv[i], kConvWarps);
-      mbar_init(&bar_p[i], kWork / 32);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar_full[i], kConvWarps);
+      mbar_init(&bar_free[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar_list[i], 1);
-      mbar_init(&bar_free[i], 1);
+      mbar_init(&bar_used[i], 1);
     }
-    mbar_init(&bar_q0, kWork / 32);
-    mbar_init(&bar_q, kConvWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_qk[i], 1);
+      mbar_init(&bar_p[i], kWork / 32);
+      mbar_init(&bar_pv[i], 1);
+    }
+    mbar_init(&bar_q, 1);
     mbar_init(&bar_drain, 2);
     abort_s = 0;
     fence_mbar_init();
@@ -439,17 +451,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   volatile int* const abort = &abort_s;
   bool ok = true;
 
+  // The items that pass through the slots: for each segment its queries, then
+  // its tiles.
+  struct Slot {
+    int i = 0;             // slot of the next item
+    uint32_t parity = 0;   // of the slot's round
+    __device__ void next() {
+      if (++i == kSlots) {
+        i = 0;
+        parity ^= 1u;
+      }
+    }
+  } slot;
+
   if (ntiles == 0) {
     if (tid == 0 && p.comb) p.comb[blockIdx.x] = make_int2(-1, 0);
   } else if (warp >= kConvWarp0 && warp < kQkWarp) {
     // ======================= converter warps ==================================
     const int w = warp - kConvWarp0;
-    const int r8 = lane & 7, g4 = lane >> 3;
-    struct Oct {  // lane: token r8 of the group, code groups g4, g4 + 4, ..
+    // Lane 4 r + g: row r of the warp's group of 8, code groups g, g + 4, ..
+    // (four lanes in a row read 64 contiguous bytes: eight wavefronts a load
+    // where the transposed order took 37).
+    const int r8 = lane >> 2, g4 = lane & 3;
+    struct Oct {
       uint4 c[4], sc;
       bool valid;
       int bits;
     } raw;
+    int seg = 0, round = 0;  // segments begun; items passed, up to kSlots
+    auto wait_free = [&] {   // the slot's last item is done with
+      if (round < kSlots)
+        ++round;
+      else
+        ok &= warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort);
+    };
     auto load = [&](int t) {  // the codes and scales of tile t's group
       ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
       const int pos = ok ? pos_s[t % kRing][w * kOct + r8] : -1;
@@ -466,20 +501,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         for (int k = 0; k < 4; ++k) raw.c[k] = src[4 * k + g4];
       }
     };
-    int seg = 0;  // segments begun before this one
-    auto step = [&](const Oct& o, int t) {
-      const int buf = t & 1;
-      if ((o.bits & kFirst) && t > 0) {
-        // a later segment begins: this warp's share of the new queries, once
-        // the last product with the old ones is done (and before its arrival
-        // for the tile, which publishes hs_s to the workers)
+    load(0);
+#pragma unroll 1
+    for (int t = 0; t < ntiles; ++t) {
+      // A group's registers are copied (which waits for its loads) before the
+      // next group's loads are issued: with two sets in turn the wait for the
+      // older loads also waited for the newer ones, 1,300 cycles a group.
+      const Oct o = raw;
+      const int unit = meta_s[t % kRing].unit;
+      if (t + 1 < ntiles) load(t + 1);
+      if (o.bits & kFirst) {  // the segment's queries go first (the workers take them to TMEM)
+        load_q<kSparse>(p, unit, slot_u + slot.i * kSlotBytes, hs_s[seg & 3], w, wait_free);
         ++seg;
-        load_q<kSparse>(p, meta_s[t % kRing].unit, q_u, hs_s[seg & 3], w, kConvWarps, [&] {
-          ok &= warp_wait(&bar_qk[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
-        });
-        fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_q);
+        if (lane == 0) mbar_arrive(&bar_full[slot.i]);
+        slot.next();
       }
       // the row's largest exponent byte but 255 (a NaN group): bytes + 1 mod
       // 256, a word of four per lane
@@ -487,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       const uint32_t mine = g4 < 2 ? (g4 == 0 ? sw[0] : sw[1]) : (g4 == 2 ? sw[2] : sw[3]);
       uint32_t mx = __vmaxu2(((mine & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu,
                              (((mine >> 8) & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
-      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // biased exponent of the row, kept where 2^E and 2^-E are normal
       const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
       __half2 s2[4];
@@ -500,60 +536,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         if (b == kFp4NanByte) s = __ushort_as_half(0x7E00);
         s2[k] = __half2half2(s);
       }
+      wait_free();
       const int row = w * kOct + r8;
-      const uint32_t base = kv_u + (buf * kTT + row) * 128;
-      uint32_t v[16 * kAhead];
-      auto to_half = [&](int k, uint32_t* dst) {
-        const uint32_t in[4] = {o.c[k].x, o.c[k].y, o.c[k].z, o.c[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t h[4];
-          fp4x8_to_half2x4(in[i], h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[4 * i + e] = h2_bits(__hmul2(*reinterpret_cast<__half2*>(&h[e]), s2[k]));
-        }
-      };
-      auto put = [&](int k, const uint32_t* src) {
-        const int g = 4 * k + g4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sts128(base + (g >> 1) * kKVRegion + (((4 * (g & 1) + i) ^ r8) << 4), src[4 * i],
-                 src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
-      };
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) to_half(k, v + 16 * k);
-      if (t >= 2) ok &= warp_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
-      if (lane < kOct)
-        te_s[buf][row] = o.valid ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
-                                 : make_float2(1.f, -INFINITY);
+      if (g4 == 0)
+        te_s[slot.i][row] = o.valid
+                                ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
+                                : make_float2(1.f, -INFINITY);
       // tokens up to the next multiple of 16 take part in the products
       if (w * kOct < max(16, ((o.bits & 0xFF) + 15) & ~15)) {
+        // Lanes with g4 >= 2 store a group's four 16-byte pieces in the order
+        // 2, 3, 0, 1: the eight lanes of a store phase (two rows, four groups)
+        // then meet eight different bank groups.
+        const uint32_t base = slot_u + slot.i * kSlotBytes + row * 128 + (g4 >> 1) * kRegion +
+                              (((4 * (g4 & 1)) ^ r8 ^ (g4 & 2)) << 4);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) put(k, v + 16 * k);
+        for (int k = 0; k < 4; ++k) {
+          const bool swap = (g4 & 2) != 0;
+          const uint32_t in[4] = {swap ? o.c[k].z : o.c[k].x, swap ? o.c[k].w : o.c[k].y,
+                                  swap ? o.c[k].x : o.c[k].z, swap ? o.c[k].y : o.c[k].w};
 #pragma unroll
-        for (int k = kAhead; k < 4; ++k) {
-          uint32_t h[16];
-          to_half(k, h);
-          put(k, h);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+            fp4x8_to_half2x4(in[i], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = h2_bits(__hmul2(*reinterpret_cast<__half2*>(&h[e]), s2[k]));
+            sts128((base ^ (i << 4)) + 2 * k * kRegion, h[0], h[1], h[2], h[3]);
+          }
         }
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_kv[buf]);
-    };
-    // A group's registers are copied (which waits for its loads) before the
-    // next group's loads are issued: with two sets in turn the wait for the
-    // older loads also waited for the newer ones, 1,300 cycles a group.
-    // A group's registers are copied (which waits for its loads) before the
-    // next group's loads are issued: with two sets in turn the wait for the
-    // older loads also waited for the newer ones, 1,300 cycles a group.
-    load(0);
-#pragma unroll 1
-    for (int t = 0; t < ntiles; ++t) {
-      const Oct cur = raw;
-      if (t + 1 < ntiles) load(t + 1);
-      step(cur, t);
+      if (lane == 0) mbar_arrive(&bar_full[slot.i]);
+      slot.next();
     }
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // ======================= MMA issue ========================================
@@ -562,54 +576,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     const uint32_t el = elect_lane();
     const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
     if (warp == kQkWarp) {
-      const uint32_t q_lo = desc_lo(q_u, 16);
       int seg = 0;  // segments begun
 #pragma unroll 1
-      for (int t = 0; t < ntiles && ok; ++t) {
+      for (int t = 0; t < ntiles; ++t) {
         // S buffer t & 1 is free once the softmax of tile t-2 has read it
         if (t >= 2) ok &= warp_wait(&bar_p[t & 1], ((t - 2) >> 1) & 1, abort);
-        ok &= warp_wait(&bar_kv[t & 1], (t >> 1) & 1, abort);
+        ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
         const int bits = meta_s[t % kRing].bits;
-        if (bits & kFirst) {
-          ok &= seg == 0 ? warp_wait(&bar_q0, 0, abort) : warp_wait(&bar_q, (seg - 1) & 1, abort);
-          ++seg;
-        }
+        if (bits & kFirst) slot.next();  // the queries
+        ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+        if (bits & kFirst) ok &= warp_wait(&bar_q, seg++ & 1, abort);
         if (!ok) break;  // uniform
         tc_fence_after();
         const uint32_t n16 = static_cast<uint32_t>(max(16, ((bits & 0xFF) + 15) & ~15));
         const uint32_t idesc = kIdescF16 | ((n16 >> 3) << 17);
-        const uint32_t d = tm0 + (16u << 16) + 256 + 64 * (t & 1);
-        const uint32_t k_lo = desc_lo(kv_u + (t & 1) * kTT * 128, 16);
+        const uint32_t d = tm0 + kColS + 64 * (t & 1);
+        const uint32_t k_lo = desc_lo(slot_u + slot.i * kSlotBytes, 16);
 #pragma unroll
         for (int k = 0; k < kLatent / 16; ++k)
-          umma_f16<kDescHi, kDescHi>(el, d, q_lo + (((k >> 2) * kRegion + (k & 3) * 32) >> 4),
-                                     k_lo + (((k >> 2) * kKVRegion + (k & 3) * 32) >> 4), idesc,
-                                     k > 0 ? 1u : 0u);
+          umma_f16_ta<kDescHi>(el, d, tm0 + 8 * k, k_lo + (((k >> 2) * kRegion + (k & 3) * 32) >> 4),
+                               idesc, k > 0 ? 1u : 0u);
         umma_commit_elect(&bar_qk[t & 1]);
+        slot.next();
       }
     } else {
 #pragma unroll 1
-      for (int t = 0; t < ntiles && ok; ++t) {
-        ok &= warp_wait(&bar_kv[t & 1], (t >> 1) & 1, abort);
+      for (int t = 0; t < ntiles; ++t) {
+        ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
         const int bits = meta_s[t % kRing].bits;
         const int ks = max(1, ((bits & 0xFF) + 15) >> 4);
+        if (bits & kFirst) slot.next();  // the queries
         ok &= warp_wait(&bar_p[t & 1], (t >> 1) & 1, abort);
         if (!ok) break;  // uniform
         tc_fence_after();
         const uint32_t p_lo = desc_lo(p_u + (t & 1) * kPBytes, 16);
-        const uint32_t c_lo = desc_lo(kv_u + (t & 1) * kTT * 128, kKVRegion);
+        const uint32_t c_lo = desc_lo(slot_u + slot.i * kSlotBytes, kRegion);
 #pragma unroll
         for (int nh = 0; nh < 2; ++nh) {
 #pragma unroll
           for (int k = 0; k < kTT / 16; ++k)
             if (k < ks)
-              umma_f16<kDescHi, kDescHi>(el, tm0 + (static_cast<uint32_t>(16 * nh) << 16),
-                                         p_lo + (k * 32 >> 4),
-                                         c_lo + ((nh * 4 * kKVRegion + k * 16 * 128) >> 4), kIdescPV,
-                                         (!(bits & kFirst) || k > 0) ? 1u : 0u);
+              umma_f16<kDescHi>(el, tm0 + (16u << 16) + 256 * nh, p_lo + (k * 32 >> 4),
+                                c_lo + ((nh * 4 * kRegion + k * 16 * 128) >> 4), kIdescPV,
+                                (!(bits & kFirst) || k > 0) ? 1u : 0u);
         }
         umma_commit_elect(&bar_pv[t & 1]);
-        umma_commit_elect(&bar_free[t % kRing]);
+        umma_commit_elect(&bar_free[slot.i]);
+        umma_commit_elect(&bar_used[t % kRing]);
+        slot.next();
       }
     }
     // every MMA issued completes before TMEM is released
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll 1
     for (int t = 0; t < ntiles && ok; ++t) {
       const int slot = t % kRing;
-      if (t >= kRing) ok &= warp_wait(&bar_free[slot], (t / kRing - 1) & 1, abort);
+      if (t >= kRing) ok &= warp_wait(&bar_used[slot], (t / kRing - 1) & 1, abort);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         int pos = fixed[i];
@@ -702,24 +716,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     // ======================= workers ==========================================
     const int qd = warp & 3, th = warp >> 2, half = lane >> 4;
     const int m = qd * 16 + (lane & 15);  // this thread's (row, head) pair of the unit
-    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
+    const uint32_t tm_q = tmem + (static_cast<uint32_t>(qd * 32) << 16);  // this lane quarter
     const int hpr = min(p.heads, kM);
-    load_q<kSparse>(p, part.u0, q_u, hs_s[0], warp, kWork / 32, [] {});
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar_q0);
-    ok &= warp_wait(&bar_q0, 0, abort);
-    int seg = -1, row_lim = 0;
+    int seg = 0, row_lim = 0;
     int64_t out_row = -1;  // row of out of this thread, or -1
     float hs = 0.f, m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1
     for (int t = 0; t < ntiles; ++t) {
       const int buf = t & 1;
-      ok &= warp_wait(&bar_kv[buf], (t >> 1) & 1, abort);
+      ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
       const TileMeta tm = meta_s[t % kRing];
+      ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
       if (tm.bits & kFirst) {
-        ++seg;
+        // ---- the segment's queries: from their slot to TMEM ------------------
         hs = hs_s[seg & 3][m];
+        ++seg;
         m_run = -INFINITY;
         l_run = 0.f;
         const UnitRows ur = unit_rows<kSparse>(p, tm.unit);
@@ -729,24 +740,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         // rows of one unit may see different numbers of tokens
         row_lim = !kSparse && p.rows_per_unit > 1 ? (mine ? clamp_len(p, ur.row0 + rr) : 0)
                                                   : 0x7fffffff;
+        // (the copy runs over the other half of the lanes, which hold O: both
+        // warps of the quarter have read the last segment's)
+        tc_fence_before();
+        pair_sync(qd);
+        tc_fence_after();
+#pragma unroll 1
+        for (int r = 4 * th; r < 4 * th + 4; ++r) {  // 64 dims: 32 columns
+          const uint32_t src = slot_u + slot.i * kSlotBytes + r * kRegion + m * 128;
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[4 * c]), "=r"(v[4 * c + 1]), "=r"(v[4 * c + 2]), "=r"(v[4 * c + 3])
+                         : "r"(src + ((c ^ (m & 7)) << 4)));
+          tmem_st_x32(tm_q + 32 * r, v);
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 5, 256;" ::: "memory");  // every worker's part is there
+        if (tid == 0) {
+          mbar_arrive(&bar_q);
+          mbar_arrive(&bar_free[slot.i]);
+        }
+        slot.next();
+        ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
       }
-      const float4* te = reinterpret_cast<const float4*>(&te_s[buf][32 * th + 16 * half]);
+      const float4* te = reinterpret_cast<const float4*>(&te_s[slot.i][32 * th + 16 * half]);
       float4 e2[8];  // (2^E, E) of this thread's 16 tokens
 #pragma unroll
       for (int i = 0; i < 8; ++i) e2[i] = te[i];
+      slot.next();
+      // P buffer t & 1 is free once PV(t-2) is done
+      if (t >= 2) ok &= warp_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
       ok &= warp_wait(&bar_qk[buf], (t >> 1) & 1, abort);
       tc_fence_after();
       float z[16];
       {
-        // lanes 16-31 receive the 32 logits of their head in this warp's half
-        // of the tile; tokens 0-15 of it go to the partner lane
+        // lanes 0-15 receive the 32 logits of their head in this warp's half
+        // of the tile; tokens 16-31 of it go to the partner lane
         uint32_t a[32];
-        tmem_ld_x32_async(tmem + lane_base + 256 + 64 * buf + 32 * th, a);
+        tmem_ld_x32_async(tm_q + kColS + 64 * buf + 32 * th, a);
         tmem_ld_wait_regs<32>(a);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const uint32_t v = __shfl_xor_sync(0xffffffffu, a[i], 16);
-          z[i] = __uint_as_float(half ? a[16 + i] : v);
+          const uint32_t v = __shfl_xor_sync(0xffffffffu, a[16 + i], 16);
+          z[i] = __uint_as_float(half ? v : a[i]);
         }
       }
       uint32_t tf[16];
@@ -793,22 +831,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       pair_sync(qd);
       mt = fmaxf(mt, red_m[buf][th ^ 1][m]);
       const bool raise = mt > m_run + kLazy || (m_run == -INFINITY && mt > m_run);
-      if (__any_sync(0xffffffffu, raise)) {
-        // (the same decision in both warps of the pair)
+      if (__any_sync(0xffffffffu, raise)) {  // (the same in both warps of the pair)
         if (raise) {
           if (m_run != -INFINITY) alpha = ex2(m_run - mt);
           m_run = mt;
         }
         if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at a segment's first tile)
+          // O is scaled in place.  The stores also rewrite the other lanes
+          // (queries, logits) with what they hold, so the products in flight
+          // are waited for: PV(t-1), and QK(t+1) if the segment goes on.
           ok &= warp_wait(&bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
+          if (!(tm.bits & kLast))
+            ok &= warp_wait(&bar_qk[(t + 1) & 1], ((t + 1) >> 1) & 1, abort);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 128 * th; c < 128 * th + 128; c += 32) {
-            float v[32];
-            tmem_ld_32x32b_x32(tmem + lane_base + c, v);
+          for (int c = 256 * th; c < 256 * th + 256; c += 32) {
+            uint32_t v[32];
+            tmem_ld_x32_async(tm_q + c, v);
+            tmem_ld_wait_regs<32>(v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= alpha;
-            tmem_st_x32(tmem + lane_base + c, v);
+            for (int i = 0; i < 32; ++i)
+              v[i] = half ? __float_as_uint(__uint_as_float(v[i]) * alpha) : v[i];
+            tmem_st_x32(tm_q + c, v);
           }
         }
         weights();
@@ -816,8 +860,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
       lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
       l_run = fmaf(l_run, alpha, lsum);  // this warp's half of the tokens
-      // P buffer t & 1 is free: the converters refilled latent buffer t & 1,
-      // so PV(t-2) is done
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int piece = 4 * th + 2 * half + c;
@@ -830,51 +872,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       if (lane == 0) mbar_arrive(&bar_p[buf]);
       if (!(tm.bits & kLast)) continue;
 
-      // ---- the segment's output --------------------------------------------
+      // ---- the segment's output (in lanes 16-31; a warp has 256 dims) --------
       if (half == 0) red_l[th][m] = l_run;
       pair_sync(qd);
       l_run += red_l[th ^ 1][m];
       ok &= warp_wait(&bar_pv[buf], (t >> 1) & 1, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
-      if ((tm.bits & (kHead | kTail)) == (kHead | kTail)) {
-        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      const bool whole = (tm.bits & (kHead | kTail)) == (kHead | kTail);
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      const int part_slot = 2 * blockIdx.x + ((tm.bits & kHead) ? 1 : 0);
+      float4* part = p.part_o + static_cast<int64_t>(part_slot) * (kPartFloats / 4) + 16 * warp +
+                     (lane & 15);
 #pragma unroll 1
-        for (int c0 = 128 * th; c0 < 128 * th + 128; c0 += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(tmem + lane_base + c0, v);
-          if (out_row >= 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kLatent + 256 * half + c0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 h2 =
-                    __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
-                o[k] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
-        }
-        if (p.lse && out_row >= 0 && half == 0 && th == 0)
-          p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
-                                        : -INFINITY;
-      } else {
-        const int slot = 2 * blockIdx.x + ((tm.bits & kHead) ? 1 : 0);
-        float4* dst = p.part_o + static_cast<int64_t>(slot) * (kPartFloats / 4) + tid;
-#pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(tmem + lane_base + 128 * th + c0, v);
+      for (int c0 = 0; c0 < 256; c0 += 32) {
+        float v[32];
+        tmem_ld_32x32b_x32(tm_q + 256 * th + c0, v);
+        if (half == 0) continue;
+        if (!whole) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[(c0 / 4 + i) * kWork] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            part[(c0 / 4 + i) * (kWork / 2)] =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else if (out_row >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kLatent + 256 * th + c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 h2 =
+                  __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+              o[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
-        if (half == 0 && th == 0) p.part_ml[slot * kM + m] = make_float2(ref_out, l_run);
       }
-      tc_fence_before();  // O is read before the next segment's first PV
+      if (half == 0 && th == 0) {
+        if (!whole)
+          p.part_ml[part_slot * kM + m] = make_float2(ref_out, l_run);
+        else if (p.lse && out_row >= 0)
+          p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
+                                        : -INFINITY;
+      }
+      tc_fence_before();  // O is read before the next segment's queries and first PV
     }
   }
   if (!ok && lane == 0) atomicExch(&g_device_error, kErrWaitTimeout);
@@ -885,7 +927,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 }
 
 // Joins the parts of the units that several CTAs shared: block (c, y) the unit
-// whose first part CTA c left, four dims of every pair for piece y of 32.
+// whose first part CTA c left, pieces 2y and 2y + 1 of 64 (four dims in each of
+// a pair's two halves).
 template <bool kSparse>
 __global__ void __launch_bounds__(kWork) k_attn_fp4_combine(const KParams p) {
   __shared__ float w_s[kMaxGrid][kM];
@@ -928,13 +971,13 @@ __global__ void __launch_bounds__(kWork) k_attn_fp4_combine(const KParams p) {
     }
   }
   __syncthreads();
-  const int warp = tid >> 5, lane = tid & 31;
-  const int qd = warp & 3, th = warp >> 2, half = lane >> 4, m = qd * 16 + (lane & 15);
+  const int wt = tid & 127, piece4 = 2 * piece + (tid >> 7);
+  const int qd = (wt >> 4) & 3, th = wt >> 6, m = qd * 16 + (wt & 15);
   const UnitRows ur = unit_rows<kSparse>(p, cb.x);
   const int hpr = min(p.heads, kM), rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
   if (rr >= ur.nrows || h >= p.heads) return;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* src = p.part_o + piece * kWork + tid;
+  const float4* src = p.part_o + piece4 * (kWork / 2) + wt;
 #pragma unroll 8
   for (int i = 0; i < parts; ++i) {
     const float4 v = src[static_cast<int64_t>(slot(i)) * (kPartFloats / 4)];
@@ -948,7 +991,7 @@ __global__ void __launch_bounds__(kWork) k_attn_fp4_combine(const KParams p) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(ur.row0 + rr) * p.heads + h) * kLatent +
-                            256 * half + 128 * th + 4 * piece) =
+                            256 * th + 4 * piece4) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
@@ -973,7 +1016,7 @@ cudaError_t launch(const AttnFp4Plan& pl, const KParams& p, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (pl.ws_bytes > 0) {
-    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, kLatent / 16), dim3(kWork), 0, stream,
+    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, 32), dim3(kWork), 0, stream,
                   true, 1, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
