@@ -55,9 +55,8 @@ constexpr int kConvWarp0 = 8;    // converter warps 8-15
 constexpr int kConvWarps = 8;
 constexpr int kQkWarp = 16;      // MMA issue
 constexpr int kPvWarp = 17;
-constexpr int kListWarp = 18;    // token positions, L2 prefetch
+constexpr int kListWarp = 18;    // token lists, loads of codes and scales
 constexpr int kThreads = 19 * 32;  // 96 registers a thread
-constexpr int kRing = 8;         // tiles the list warp is ahead of a finished one
 constexpr int kTT = 64;          // tokens per tile
 constexpr int kM = 64;           // (row, head) pairs per unit (MMA M)
 constexpr int kOct = 8;          // tokens of a tile that a converter warp takes
@@ -102,13 +101,14 @@ struct KParams {
 // A tile as the list warp describes it to the other roles.
 struct __align__(16) TileMeta {
   int unit;
-  int tile;  // index in the unit
-  int bits;  // tokens in its part of the list (0..64), and flags
-  int64_t tok0;  // first cache token of its sequence
+  int tile;           // index in the unit
+  int bits;           // tokens in its part of the list (0..64), and flags
+  uint32_t valid[2];  // a bit per token that has a row in the cache
   __device__ int ntok() const { return bits & 0xFF; }
 };
-// first, last tile of its segment; the segment has the unit's first, last tile
-enum : int { kFirst = 256, kLast = 512, kHead = 1024, kTail = 2048 };
+// first, last tile of its segment; the segment has the unit's first, last tile;
+// not a tile but its segment's queries
+enum : int { kFirst = 256, kLast = 512, kHead = 1024, kTail = 2048, kQueries = 4096 };
 
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -116,11 +116,14 @@ __device__ __forceinline__ void fence_proxy_async() {
 __device__ __forceinline__ void pair_sync(int qd) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
 }
-// Waits for a phase with the thread suspended until it completes (or 1 ms has
-// passed: then the limit and the abort flag are looked at, as in mbar_wait).
-__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// A warp's wait for a phase, its threads suspended until the phase completes
+// (or 1 ms has passed: then the abort flag and the limit of 2^32 - 2^28 clocks,
+// about two seconds, are looked at).  On a timeout it sets the abort flag and
+// the error word.  The same result for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t addr = smem_u32(bar);
-  uint64_t t0 = 0;
+  const uint32_t t0 = clock();
+  bool r = true;
   for (;;) {
     uint32_t done;
     asm volatile(
@@ -130,21 +133,25 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volat
         : "=r"(done)
         : "r"(addr), "r"(parity), "r"(1000000)
         : "memory");
-    if (done) return true;
-    if (*abort) return false;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
+    if (done) break;
+    if (*abort || static_cast<uint32_t>(clock()) - t0 > 0xF0000000u) {
+      if (!*abort) atomicExch(&g_device_error, kErrWaitTimeout);
       *abort = 1;
-      atomicExch(&g_device_error, kErrWaitTimeout);
-      return false;
+      r = false;
+      break;
     }
   }
-}
-// A warp's wait; the same result for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool r = mbar_sleep(bar, parity, abort);
   return __all_sync(0xffffffffu, r);
+}
+// Untiled bulk copy of global memory to shared memory (16-byte aligned, a
+// multiple of 16 bytes), completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 // Asks `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
 __device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
@@ -159,6 +166,12 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                                        uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
                : "memory");
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -239,13 +252,13 @@ struct UnitRows {
 template <bool kSparse>
 __device__ __forceinline__ UnitRows unit_rows(const KParams& p, int u) {
   UnitRows r;
-  const int rest = u / p.groups;
-  r.hg = u - rest * p.groups;
+  const int rest = u >> (p.groups - 1);  // one or two groups
+  r.hg = u & (p.groups - 1);
   if (kSparse) {
     r.row0 = rest;
     r.nrows = 1;
   } else {
-    const int s = rest / p.rgs, rg = rest - s * p.rgs;
+    const int s = p.rgs == 1 ? rest : rest / p.rgs, rg = rest - s * p.rgs;
     r.row0 = s * p.per_seq + rg * p.rows_per_unit;
     r.nrows = min(p.rows_per_unit, p.per_seq - rg * p.rows_per_unit);
   }
@@ -276,67 +289,60 @@ __device__ __forceinline__ int tiles_of(int S) { return max(1, (S + kTT - 1) / k
 
 // The part of the tile sequence a CTA owns, as every thread learns it.
 struct Part {
-  int64_t begin, end, quota;
-  int u0;        // unit of tile `begin`
-  int64_t off0;  // first tile of that unit
+  int begin, end, quota;
+  int u0, off0;  // unit of tile `begin`, its first tile
 };
 
-// Scans the units' tile counts (every thread of the block calls this).
+// Scans the units' tile counts (every thread of the block calls this).  The
+// loops stay rolled: the code runs once, and each of its lines is fetched for
+// that.
 template <bool kSparse>
-__device__ Part plan_part(const KParams& p, int64_t* scratch /* [kThreads / 32 + 2] */) {
+__device__ __forceinline__ Part plan_part(const KParams& p, int* scratch /* [kThreads / 32 + 2] */) {
+  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Part part;
-  int64_t sum = 0;
-  int first = 0;  // tiles of unit tid, kept for the scan
+  int sum = 0, first = 0;  // tiles of unit tid, kept for the scan
+#pragma unroll 1
   for (int u = tid; u < p.units; u += kThreads) {
     const int t = tiles_of(load_unit<kSparse>(p, u).S);
     if (u == tid) first = t;
     sum += t;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) scratch[warp] = sum;
   __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
+  const int total = __reduce_add_sync(0xffffffffu, lane < kWarps ? scratch[lane] : 0);
   __syncthreads();
-  const int64_t g = gridDim.x;
-  part.quota = max((total + g - 1) / g, static_cast<int64_t>(p.min_tiles));
-  part.begin = part.quota * blockIdx.x;
-  part.end = min(part.begin + part.quota, total);
+  const int g = static_cast<int>(gridDim.x);
+  part.quota = max((total - 1) / g + 1, p.min_tiles);
+  const int64_t begin = static_cast<int64_t>(part.quota) * blockIdx.x;
+  part.begin = static_cast<int>(begin < total ? begin : total);
+  part.end = min(part.begin + min(part.quota, total - part.begin), total);
   part.u0 = 0;
   part.off0 = 0;
-  int64_t base = 0;
+  int base = 0;
+#pragma unroll 1
   for (int b = 0; part.begin < total; b += kThreads) {  // uniform; ends where the unit is found
     const int u = b + tid;
-    int64_t t = 0;
+    int t = 0;
     if (u < p.units) t = b == 0 ? first : tiles_of(load_unit<kSparse>(p, u).S);
-    int64_t inc = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
+    const int inc = warp_incl_scan(t);
     if (lane == 31) scratch[warp] = inc;
     __syncthreads();
-    int64_t before = base, all = base;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += scratch[w];
-      all += scratch[w];
-    }
-    const int64_t off = before + inc - t;
-    if (t > 0 && off <= part.begin && part.begin < off + t) {
-      scratch[kThreads / 32] = u;
-      scratch[kThreads / 32 + 1] = off;
+    const int ws = warp_incl_scan(lane < kWarps ? scratch[lane] : 0);
+    const int before = __shfl_sync(0xffffffffu, ws, warp > 0 ? warp - 1 : 0);
+    const int off = base + (warp > 0 ? before : 0) + inc - t;
+    base += __shfl_sync(0xffffffffu, ws, kWarps - 1);
+    if (t > 0 && off <= part.begin && part.begin - off < t) {
+      scratch[kWarps] = u;
+      scratch[kWarps + 1] = off;
     }
     __syncthreads();
-    if (part.begin < all) {
-      part.u0 = static_cast<int>(scratch[kThreads / 32]);
-      part.off0 = scratch[kThreads / 32 + 1];
+    if (part.begin < base) {
+      part.u0 = scratch[kWarps];
+      part.off0 = scratch[kWarps + 1];
       break;
     }
-    base = all;
-    if (b + kThreads >= p.units) break;  // (cannot happen: begin < total)
   }
   return part;
 }
@@ -344,15 +350,13 @@ __device__ Part plan_part(const KParams& p, int64_t* scratch /* [kThreads / 32 +
 // ---- queries ------------------------------------------------------------------
 // Rows w, w + 8, .. of the unit's 64 query rows to a shared-memory slot as
 // fp16, each scaled by a power of two; hs[m] is what a product with it is
-// multiplied by.  `wait` is called between the first loads and the first store.
-template <bool kSparse, typename Wait>
-__device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t slot, float* hs, int w,
-                                       Wait wait) {
+// multiplied by.
+template <bool kSparse>
+__device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t slot, float* hs, int w) {
   constexpr int nw = kConvWarps;
   const int lane = threadIdx.x & 31;
   const UnitRows r = unit_rows<kSparse>(p, u);
   const int hpr = min(p.heads, kM);  // heads of a row in the unit
-  bool waited = false;
 #pragma unroll 1
   for (int m0 = w; m0 < kM; m0 += 4 * nw) {
     uint4 v[4][2];
@@ -368,8 +372,6 @@ __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t slot, f
         v[i][1] = src[32 + lane];
       }
     }
-    if (!waited) wait();
-    waited = true;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = m0 + i * nw;
@@ -404,28 +406,25 @@ template <bool kSparse>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   extern __shared__ uint8_t dyn[];
   const uint32_t slot_u = (smem_u32(dyn) + 1023) & ~1023u, p_u = slot_u + kSlots * kSlotBytes;
-  __shared__ uint64_t bar_full[kSlots], bar_free[kSlots];  // slots: filled, given back
-  __shared__ uint64_t bar_list[kRing], bar_used[kRing];    // list ring: filled, tile done
-  __shared__ uint64_t bar_qk[2], bar_p[2], bar_pv[2];      // S(t), P(t), O of tile t & 1 ready
-  __shared__ uint64_t bar_q, bar_drain;                    // queries in TMEM; all MMAs done
-  __shared__ TileMeta meta_s[kRing];
-  __shared__ int pos_s[kRing][kTT];  // token positions in the sequence, -1: nothing there
+  __shared__ uint64_t bar_raw[kSlots];   // slots: codes and scales have landed
+  __shared__ uint64_t bar_full[kSlots];  // converted
+  __shared__ uint64_t bar_free[kSlots];  // given back
+  __shared__ uint64_t bar_qk[2], bar_p[2], bar_pv[2];  // S(t), P(t), O of tile t & 1 ready
+  __shared__ uint64_t bar_q, bar_drain;                // queries in TMEM; all MMAs done
+  __shared__ TileMeta meta_s[kSlots];
   __shared__ __align__(16) float2 te_s[kSlots][kTT];  // (2^E, E) per token; (1, -inf): nothing there
   __shared__ float hs_s[4][kM];                       // per segment, mod 4
   __shared__ float red_m[2][2][kM], red_l[2][kM];
-  __shared__ int64_t scratch[kThreads / 32 + 2];
+  __shared__ int scratch[kThreads / 32 + 2];
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar_raw[i], 1);
       mbar_init(&bar_full[i], kConvWarps);
       mbar_init(&bar_free[i], 1);
-    }
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bar_list[i], 1);
-      mbar_init(&bar_used[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_qk[i], 1);
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   }
   pdl_trigger();
   const Part part = plan_part<kSparse>(p, scratch);
-  const int ntiles = part.begin < part.end ? static_cast<int>(part.end - part.begin) : 0;
+  const int ntiles = part.end - part.begin;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -468,99 +467,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     if (tid == 0 && p.comb) p.comb[blockIdx.x] = make_int2(-1, 0);
   } else if (warp >= kConvWarp0 && warp < kQkWarp) {
     // ======================= converter warps ==================================
+    // The raw rows of a warp's 8 tokens lie where their fp16 rows will: blocks
+    // of 4 tokens (1 KiB of codes) in its 1 KiB of the regions 0 and 1, the
+    // scales (128 B) in region 2.  Lane 4 r + g has row r, code groups g, g +
+    // 4, ..; odd rows take the groups in pairs swapped (g + 4 first), so that
+    // the eight lanes of a load phase meet different banks.
     const int w = warp - kConvWarp0;
-    // Lane 4 r + g: row r of the warp's group of 8, code groups g, g + 4, ..
-    // (four lanes in a row read 64 contiguous bytes: eight wavefronts a load
-    // where the transposed order took 37).
     const int r8 = lane >> 2, g4 = lane & 3;
-    struct Oct {
-      uint4 c[4], sc;
-      bool valid;
-      int bits;
-    } raw;
-    int seg = 0, round = 0;  // segments begun; items passed, up to kSlots
-    auto wait_free = [&] {   // the slot's last item is done with
-      if (round < kSlots)
-        ++round;
-      else
-        ok &= warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort);
-    };
-    auto load = [&](int t) {  // the codes and scales of tile t's group
-      ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
-      const int pos = ok ? pos_s[t % kRing][w * kOct + r8] : -1;
-      raw.bits = meta_s[t % kRing].bits;
-      raw.valid = pos >= 0;
-      raw.sc = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) raw.c[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (raw.valid) {
-        const int64_t at = meta_s[t % kRing].tok0 + pos;
-        raw.sc = *reinterpret_cast<const uint4*>(p.scales + at * kFp4Groups);
-        const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * kFp4CodeBytes);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) raw.c[k] = src[4 * k + g4];
-      }
-    };
-    load(0);
+    const bool odd = (r8 & 1) != 0, swap = (g4 & 2) != 0;
+    const uint32_t raw_off = w * 1024 + (r8 >> 2) * kRegion + (r8 & 3) * 256 + g4 * 16 + (odd ? 64 : 0);
+    // Lanes with g4 >= 2 store a group's four 16-byte pieces in the order 2, 3,
+    // 0, 1: the eight lanes of a store phase (two rows, four groups) then meet
+    // eight different bank groups.
+    const uint32_t out_off = (w * kOct + r8) * 128 + (g4 >> 1) * kRegion +
+                             (((4 * (g4 & 1)) ^ r8 ^ (g4 & 2)) << 4) + (odd ? 2 * kRegion : 0);
+    int seg = 0;  // segments begun
 #pragma unroll 1
-    for (int t = 0; t < ntiles; ++t) {
-      // A group's registers are copied (which waits for its loads) before the
-      // next group's loads are issued: with two sets in turn the wait for the
-      // older loads also waited for the newer ones, 1,300 cycles a group.
-      const Oct o = raw;
-      const int unit = meta_s[t % kRing].unit;
-      if (t + 1 < ntiles) load(t + 1);
-      if (o.bits & kFirst) {  // the segment's queries go first (the workers take them to TMEM)
-        load_q<kSparse>(p, unit, slot_u + slot.i * kSlotBytes, hs_s[seg & 3], w, wait_free);
+    for (int t = 0; t < ntiles;) {
+      ok &= warp_wait(&bar_raw[slot.i], slot.parity, abort);
+      const uint32_t base = slot_u + slot.i * kSlotBytes;
+      const int bits = meta_s[slot.i].bits;
+      if (bits & kQueries) {  // (the workers take them to TMEM)
+        load_q<kSparse>(p, meta_s[slot.i].unit, base, hs_s[seg & 3], w);
         ++seg;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_full[slot.i]);
-        slot.next();
-      }
-      // the row's largest exponent byte but 255 (a NaN group): bytes + 1 mod
-      // 256, a word of four per lane
-      const uint32_t sw[4] = {o.sc.x, o.sc.y, o.sc.z, o.sc.w};
-      const uint32_t mine = g4 < 2 ? (g4 == 0 ? sw[0] : sw[1]) : (g4 == 2 ? sw[2] : sw[3]);
-      uint32_t mx = __vmaxu2(((mine & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu,
-                             (((mine >> 8) & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
-      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // biased exponent of the row, kept where 2^E and 2^-E are normal
-      const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
-      __half2 s2[4];
+      } else {
+        ++t;
+        const bool valid = ok && ((meta_s[slot.i].valid[w >> 2] >> (8 * (w & 3) + r8)) & 1u);
+        uint32_t c[4][4], sw[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int b = static_cast<int>((sw[k] >> (8 * g4)) & 0xFFu);
-        // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group)
-        __half s = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
-        if (b == kFp4NanByte) s = __ushort_as_half(0x7E00);
-        s2[k] = __half2half2(s);
-      }
-      wait_free();
-      const int row = w * kOct + r8;
-      if (g4 == 0)
-        te_s[slot.i][row] = o.valid
-                                ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
-                                : make_float2(1.f, -INFINITY);
-      // tokens up to the next multiple of 16 take part in the products
-      if (w * kOct < max(16, ((o.bits & 0xFF) + 15) & ~15)) {
-        // Lanes with g4 >= 2 store a group's four 16-byte pieces in the order
-        // 2, 3, 0, 1: the eight lanes of a store phase (two rows, four groups)
-        // then meet eight different bank groups.
-        const uint32_t base = slot_u + slot.i * kSlotBytes + row * 128 + (g4 >> 1) * kRegion +
-                              (((4 * (g4 & 1)) ^ r8 ^ (g4 & 2)) << 4);
+        for (int k = 0; k < 4; ++k)  // groups 4 (k ^ odd) + g4
+          lds128(base + ((raw_off + 128 * (k >> 1)) ^ (64 * (k & 1))), c[k]);
+        lds128(base + w * 1024 + 2 * kRegion + r8 * 16, sw);
+        // the row's largest exponent byte but 255 (a NaN group): bytes + 1 mod
+        // 256, a word of four per lane
+        const uint32_t mine = swap ? (g4 & 1 ? sw[3] : sw[2]) : (g4 & 1 ? sw[1] : sw[0]);
+        uint32_t mx = __vmaxu2(((mine & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu,
+                               (((mine >> 8) & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // (the raw rows are read)
+        // biased exponent of the row, kept where 2^E and 2^-E are normal
+        const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
+        if (g4 == 0)
+          te_s[slot.i][w * kOct + r8] =
+              valid ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
+                    : make_float2(1.f, -INFINITY);
+        // tokens up to the next multiple of 16 take part in the products
+        if (w * kOct < max(16, ((bits & 0xFF) + 15) & ~15)) {
+          __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool swap = (g4 & 2) != 0;
-          const uint32_t in[4] = {swap ? o.c[k].z : o.c[k].x, swap ? o.c[k].w : o.c[k].y,
-                                  swap ? o.c[k].x : o.c[k].z, swap ? o.c[k].y : o.c[k].w};
+          for (int k = 0; k < 4; ++k) {
+            const int b = static_cast<int>(((odd ? sw[k ^ 1] : sw[k]) >> (8 * g4)) & 0xFFu);
+            // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group; 0 where
+            // there is no token)
+            __half sc = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
+            if (b == kFp4NanByte) sc = __ushort_as_half(0x7E00);
+            const __half2 s2 = __half2half2(valid ? sc : __ushort_as_half(0));
+            const uint32_t dst = base + (odd ? out_off - 4 * kRegion * (k & 1) : out_off) +
+                                 2 * kRegion * k;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h[4];
-            fp4x8_to_half2x4(in[i], h);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h[4];
+              fp4x8_to_half2x4(swap ? c[k][i ^ 2] : c[k][i], h);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = h2_bits(__hmul2(*reinterpret_cast<__half2*>(&h[e]), s2[k]));
-            sts128((base ^ (i << 4)) + 2 * k * kRegion, h[0], h[1], h[2], h[3]);
+              for (int e = 0; e < 4; ++e) h[e] = h2_bits(__hmul2(*reinterpret_cast<__half2*>(&h[e]), s2));
+              sts128(dst ^ (i << 4), h[0], h[1], h[2], h[3]);
+            }
           }
         }
       }
@@ -575,39 +546,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     // loop and one elected lane issues, so the descriptors are warp-uniform.
     const uint32_t el = elect_lane();
     const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+    // A segment's first tile follows its queries, whose slot is not waited for
+    // here: the workers give it back without these warps.
+    bool fresh = true;
     if (warp == kQkWarp) {
       int seg = 0;  // segments begun
 #pragma unroll 1
-      for (int t = 0; t < ntiles; ++t) {
+      for (int t = 0; t < ntiles; ++t, slot.next()) {
+        if (fresh) {
+          slot.next();
+          ok &= warp_wait(&bar_q, seg++ & 1, abort);
+        }
         // S buffer t & 1 is free once the softmax of tile t-2 has read it
         if (t >= 2) ok &= warp_wait(&bar_p[t & 1], ((t - 2) >> 1) & 1, abort);
-        ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
-        const int bits = meta_s[t % kRing].bits;
-        if (bits & kFirst) slot.next();  // the queries
         ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
-        if (bits & kFirst) ok &= warp_wait(&bar_q, seg++ & 1, abort);
         if (!ok) break;  // uniform
+        const int bits = meta_s[slot.i].bits;
+        fresh = (bits & kLast) != 0;
         tc_fence_after();
         const uint32_t n16 = static_cast<uint32_t>(max(16, ((bits & 0xFF) + 15) & ~15));
         const uint32_t idesc = kIdescF16 | ((n16 >> 3) << 17);
         const uint32_t d = tm0 + kColS + 64 * (t & 1);
         const uint32_t k_lo = desc_lo(slot_u + slot.i * kSlotBytes, 16);
+#pragma unroll 1
+        for (int k = 0; k < kLatent / 64; ++k) {
 #pragma unroll
-        for (int k = 0; k < kLatent / 16; ++k)
-          umma_f16_ta<kDescHi>(el, d, tm0 + 8 * k, k_lo + (((k >> 2) * kRegion + (k & 3) * 32) >> 4),
-                               idesc, k > 0 ? 1u : 0u);
+          for (int i = 0; i < 4; ++i)
+            umma_f16_ta<kDescHi>(el, d, tm0 + 32 * k + 8 * i, k_lo + ((k * kRegion + i * 32) >> 4),
+                                 idesc, k + i > 0 ? 1u : 0u);
+        }
         umma_commit_elect(&bar_qk[t & 1]);
-        slot.next();
       }
     } else {
 #pragma unroll 1
-      for (int t = 0; t < ntiles; ++t) {
-        ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
-        const int bits = meta_s[t % kRing].bits;
-        const int ks = max(1, ((bits & 0xFF) + 15) >> 4);
-        if (bits & kFirst) slot.next();  // the queries
-        ok &= warp_wait(&bar_p[t & 1], (t >> 1) & 1, abort);
+      for (int t = 0; t < ntiles; ++t, slot.next()) {
+        if (fresh) slot.next();
+        ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
         if (!ok) break;  // uniform
+        const int bits = meta_s[slot.i].bits;
+        fresh = (bits & kLast) != 0;
+        const int ks = max(1, ((bits & 0xFF) + 15) >> 4);
+        ok &= warp_wait(&bar_p[t & 1], (t >> 1) & 1, abort);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t p_lo = desc_lo(p_u + (t & 1) * kPBytes, 16);
         const uint32_t c_lo = desc_lo(slot_u + slot.i * kSlotBytes, kRegion);
@@ -622,8 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         }
         umma_commit_elect(&bar_pv[t & 1]);
         umma_commit_elect(&bar_free[slot.i]);
-        umma_commit_elect(&bar_used[t % kRing]);
-        slot.next();
       }
     }
     // every MMA issued completes before TMEM is released
@@ -634,11 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     }
   } else if (warp == kListWarp) {
     // ======================= list warp ========================================
-    // The token positions of tile after tile (two tokens a lane), block ids
-    // loaded one tile ahead; the rows are asked into L2 here.
+    // Lanes i < 16 find block i of a tile (4 tokens of the list: a selected
+    // block, the partial tail, or four tokens in a row) and load its codes,
+    // lane 16 + i its scales.  Block ids are read a tile ahead, and the rows
+    // asked into L2 before the wait for the tile's slot.
     int u = part.u0;
     Unit un = load_unit<kSparse>(p, u), nxt{};
-    int t_org = static_cast<int>(part.off0 - part.begin);  // CTA tiles [t_org, t_end) are u's
+    int t_org = part.off0 - part.begin;  // CTA tiles [t_org, t_end) are u's
     int t_end = t_org + tiles_of(un.S);
     int2 comb = make_int2(-1, 0);
     int64_t tok0;
@@ -649,13 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       tok0 = static_cast<int64_t>(kSparse ? row0 : row0 / p.per_seq) * p.seq_tok;
       ids = p.idx + static_cast<int64_t>(row0) * kTopK;  // (unused when dense)
       if (t_org >= 0 && t_end > ntiles)  // the split unit that begins here
-        comb = make_int2(u, static_cast<int>((part.begin + t_end - 1) / part.quota) -
-                                static_cast<int>(blockIdx.x) + 1);
+        comb = make_int2(u, (part.begin + t_end - 1) / part.quota - static_cast<int>(blockIdx.x) + 1);
     };
-    enter_unit();
-    int b[2], fixed[2], nblk = 0;  // of the next tile: ids, or positions no id decides (-2: it does)
+    int pos = 0, nt = 0;  // of this lane's block: first token, tokens (0..4)
     TileMeta m;
-    auto request = [&](int t) {
+    auto request = [&](int t) {  // the blocks of tile t
       if (t >= t_end) {
         ++u;
         un = nxt;
@@ -665,53 +643,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       }
       m.unit = u;
       m.tile = t - t_org;
-      m.tok0 = tok0;
       m.bits = max(0, min(un.S - m.tile * kTT, kTT)) | (t == max(t_org, 0) ? kFirst : 0) |
                (t == min(t_end, ntiles) - 1 ? kLast : 0) | (t_org >= 0 ? kHead : 0) |
                (t_end <= ntiles ? kTail : 0);
-      nblk = un.n >> 2;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = m.tile * kTT + 32 * i + lane;
-        fixed[i] = j < un.S ? j : -1;
-        b[i] = -1;
-        if (kSparse && fixed[i] >= 0) {
-          if (j < un.cnt * kPool) {
-            fixed[i] = -2;
-            b[i] = ids[j >> 2];
-          } else {
-            fixed[i] = nblk * kPool + (j - un.cnt * kPool);
-          }
+      const int j = m.tile * kTT + (lane & 15) * kPool;
+      pos = j;
+      nt = max(0, min(un.S - j, kPool));
+      if (kSparse && nt > 0) {
+        if (j < un.cnt * kPool) {
+          const int b = ids[j >> 2];
+          if (b < 0 || b >= un.n >> 2)
+            nt = 0;
+          else
+            pos = b * kPool;
+        } else {
+          pos = un.n & ~(kPool - 1);
         }
       }
     };
+    enter_unit();
     request(0);
+    int round = 0;  // items passed, up to kSlots
+    auto wait_free = [&] {
+      if (round < kSlots)
+        ++round;
+      else
+        ok &= warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort);
+    };
+    uint32_t landed[kSlots];  // parity of the last load into a slot
+    int loads = 0;            // slots loaded into (bits)
 #pragma unroll 1
-    for (int t = 0; t < ntiles && ok; ++t) {
-      const int slot = t % kRing;
-      if (t >= kRing) ok &= warp_wait(&bar_used[slot], (t / kRing - 1) & 1, abort);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int pos = fixed[i];
-        if (kSparse && pos == -2) pos = b[i] < 0 || b[i] >= nblk ? -1 : b[i] * kPool + (lane & 3);
-        pos_s[slot][32 * i + lane] = pos;
-        if (kSparse && (lane & 3) == 0 && pos >= 0) {  // a block (or the partial tail's tokens)
-          const uint32_t rows = static_cast<uint32_t>(min(kPool, (m.bits & 0xFF) - 32 * i - lane));
-          l2_prefetch(p.codes + (m.tok0 + pos) * kFp4CodeBytes, rows * kFp4CodeBytes);
-          l2_prefetch(p.scales + (m.tok0 + pos) * kFp4Groups, rows * kFp4Groups);
+    for (int t = 0; t < ntiles; ++t) {
+      const bool scales = lane >= 16;
+      const uint32_t row = scales ? kFp4Groups : kFp4CodeBytes;
+      const uint8_t* src =
+          (scales ? p.scales : p.codes) + (tok0 + (nt > 0 ? pos : 0)) * static_cast<int64_t>(row);
+      if (t > 0 && nt > 0) l2_prefetch(src, nt * row);
+      if (m.bits & kFirst) {
+        wait_free();
+        if (!ok) break;  // uniform
+        if (lane == 0) {
+          meta_s[slot.i].unit = m.unit;
+          meta_s[slot.i].bits = kQueries;
+          mbar_arrive(&bar_raw[slot.i]);
         }
+        slot.next();
       }
-      if (!kSparse && lane == 0 && (m.bits & 0xFF) > 0) {
-        const uint32_t rows = static_cast<uint32_t>(m.bits & 0xFF);
-        l2_prefetch(p.codes + (m.tok0 + m.tile * kTT) * kFp4CodeBytes, rows * kFp4CodeBytes);
-        l2_prefetch(p.scales + (m.tok0 + m.tile * kTT) * kFp4Groups, rows * kFp4Groups);
+      wait_free();
+      if (!ok) break;
+      const uint32_t v = lane < 16 ? ((1u << nt) - 1u) << (4 * (lane & 7)) : 0u;
+      m.valid[0] = __reduce_or_sync(0xffffffffu, lane < 8 ? v : 0u);
+      m.valid[1] = __reduce_or_sync(0xffffffffu, lane < 8 ? 0u : v);
+      if (lane == 0) {
+        meta_s[slot.i] = m;
+        mbar_arrive_expect_tx(&bar_raw[slot.i], (__popc(m.valid[0]) + __popc(m.valid[1])) *
+                                                    (kFp4CodeBytes + kFp4Groups));
       }
-      if (lane == 0) meta_s[slot] = m;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_list[slot]);
+      if (nt > 0) {
+        const int i = lane & 15;
+        const uint32_t dst = slot_u + slot.i * kSlotBytes + (i >> 1) * 1024 +
+                             (scales ? 2 * kRegion + (i & 1) * 64 : (i & 1) * kRegion);
+        bulk_load(dst, src, nt * row, &bar_raw[slot.i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (i == slot.i) landed[i] = slot.parity;
+      loads |= 1 << slot.i;
+      slot.next();
       if (t + 1 < ntiles) request(t + 1);
     }
     if (lane == 0 && p.comb) p.comb[blockIdx.x] = comb;
+    if (!ok) {  // nothing may land once the block is gone
+      volatile int no_abort = 0;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if ((loads >> i) & 1) warp_wait(&bar_raw[i], landed[i], &no_abort);
+    }
   } else if (warp < kConvWarp0) {
     // ======================= workers ==========================================
     const int qd = warp & 3, th = warp >> 2, half = lane >> 4;
@@ -722,12 +730,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     int64_t out_row = -1;  // row of out of this thread, or -1
     float hs = 0.f, m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1
-    for (int t = 0; t < ntiles; ++t) {
+    for (int t = 0; t < ntiles;) {
       const int buf = t & 1;
-      ok &= warp_wait(&bar_list[t % kRing], (t / kRing) & 1, abort);
-      const TileMeta tm = meta_s[t % kRing];
       ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
-      if (tm.bits & kFirst) {
+      const TileMeta tm = meta_s[slot.i];
+      if (ok && (tm.bits & kQueries)) {
         // ---- the segment's queries: from their slot to TMEM ------------------
         hs = hs_s[seg & 3][m];
         ++seg;
@@ -750,10 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           const uint32_t src = slot_u + slot.i * kSlotBytes + r * kRegion + m * 128;
           uint32_t v[32];
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[4 * c]), "=r"(v[4 * c + 1]), "=r"(v[4 * c + 2]), "=r"(v[4 * c + 3])
-                         : "r"(src + ((c ^ (m & 7)) << 4)));
+          for (int c = 0; c < 8; ++c) lds128(src + ((c ^ (m & 7)) << 4), v + 4 * c);
           tmem_st_x32(tm_q + 32 * r, v);
         }
         tc_fence_before();
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           mbar_arrive(&bar_free[slot.i]);
         }
         slot.next();
-        ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+        continue;
       }
       const float4* te = reinterpret_cast<const float4*>(&te_s[slot.i][32 * th + 16 * half]);
       float4 e2[8];  // (2^E, E) of this thread's 16 tokens
@@ -870,13 +874,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_p[buf]);
+      const uint32_t pv_parity = (t >> 1) & 1;
+      ++t;
       if (!(tm.bits & kLast)) continue;
 
       // ---- the segment's output (in lanes 16-31; a warp has 256 dims) --------
       if (half == 0) red_l[th][m] = l_run;
       pair_sync(qd);
       l_run += red_l[th ^ 1][m];
-      ok &= warp_wait(&bar_pv[buf], (t >> 1) & 1, abort);
+      ok &= warp_wait(&bar_pv[buf], pv_parity, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
       const bool whole = (tm.bits & (kHead | kTail)) == (kHead | kTail);
@@ -1035,12 +1041,13 @@ AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t
   pl.rows_per_unit = sparse || heads > kM / 2 ? 1 : kM / heads;
   if (pl.rows_per_unit > per_seq) pl.rows_per_unit = per_seq;
   pl.rgs = (per_seq + pl.rows_per_unit - 1) / pl.rows_per_unit;
-  pl.units = rows / per_seq * pl.rgs * pl.groups;
+  pl.units = rows / per_seq * pl.rgs * pl.groups;  // (at most 2 x 65535)
   int64_t list = max_len;  // tokens in a list, at most
   if (sparse && list > kTopK * kPool + kPool - 1) list = kTopK * kPool + kPool - 1;
   int64_t tiles = (list + kTT - 1) / kTT;
   if (tiles < 1) tiles = 1;
   const int sms = num_sms < kMaxGrid ? num_sms : kMaxGrid;
+  if (pl.units * tiles > 0x7fffffff) return AttnFp4Plan{};  // tiles are counted in 32 bits
   pl.grid = static_cast<int>(pl.units * tiles < sms ? pl.units * tiles : sms);
   pl.min_tiles = 1;
   if (tiles > 1)  // units of one tile are never split

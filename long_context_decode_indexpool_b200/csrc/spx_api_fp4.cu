@@ -29,6 +29,7 @@ spx_status attn_fp4(const spx_dims* d, int32_t rows, int32_t per_seq, const void
       (lse && !al(lse, 4)) || (sparse && (!al(idx, 4) || !al(count, 4))))
     return SPX_ERR_INVALID_ARG;
   const AttnFp4Plan p = plan_attn_fp4(rows, per_seq, d->heads, sparse, max_len, device_sm_count());
+  if (p.grid == 0) return SPX_ERR_UNSUPPORTED;
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes || !al(ws, 16))) return SPX_ERR_WORKSPACE;
   AttnFp4Args a{};
   a.rows = rows;
@@ -90,7 +91,9 @@ spx_status spx_attn_fp4_workspace_size(const spx_dims* d, int32_t rows, int64_t 
   if (st != SPX_OK) return st;
   if (!bytes) return SPX_ERR_INVALID_ARG;
   if (rows < 1 || rows > 65535 || max_len < 0) return SPX_ERR_SHAPE;
-  *bytes = plan_attn_fp4(rows, 1, d->heads, true, max_len, device_sm_count()).ws_bytes;
+  const AttnFp4Plan p = plan_attn_fp4(rows, 1, d->heads, true, max_len, device_sm_count());
+  if (p.grid == 0) return SPX_ERR_UNSUPPORTED;
+  *bytes = p.ws_bytes;
   return SPX_OK;
 }
 
@@ -118,7 +121,10 @@ spx_status spx_latent_attn_fp4_workspace_size(const spx_dims* d, int32_t rows,
   if (!bytes) return SPX_ERR_INVALID_ARG;
   if (rows < 1 || rows > 65535 || max_len < 0) return SPX_ERR_SHAPE;
   if (rows_per_seq < 1 || rows % rows_per_seq != 0) return SPX_ERR_SHAPE;
-  *bytes = plan_attn_fp4(rows, rows_per_seq, d->heads, false, max_len, device_sm_count()).ws_bytes;
+  const AttnFp4Plan p =
+      plan_attn_fp4(rows, rows_per_seq, d->heads, false, max_len, device_sm_count());
+  if (p.grid == 0) return SPX_ERR_UNSUPPORTED;
+  *bytes = p.ws_bytes;
   return SPX_OK;
 }
 
