@@ -143,15 +143,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   }
   return __all_sync(0xffffffffu, r);
 }
-// Untiled bulk copy of global memory to shared memory (16-byte aligned, a
-// multiple of 16 bytes), completing on an mbarrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+// 16-byte asynchronous copy to shared memory, zeros where `valid` is false; the
+// second makes an mbarrier arrival of the thread's copies so far.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Asks `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
 __device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bar_raw[i], 1);
+      mbar_init(&bar_raw[i], 33);  // the list warp's lanes, and its description
       mbar_init(&bar_full[i], kConvWarps);
       mbar_init(&bar_free[i], 1);
     }
@@ -612,10 +612,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     }
   } else if (warp == kListWarp) {
     // ======================= list warp ========================================
-    // Lanes i < 16 find block i of a tile (4 tokens of the list: a selected
-    // block, the partial tail, or four tokens in a row) and load its codes,
-    // lane 16 + i its scales.  Block ids are read a tile ahead, and the rows
-    // asked into L2 before the wait for the tile's slot.
+    // Lane i < 16 finds block i of a tile (4 tokens of the list: a selected
+    // block, the partial tail, or four tokens in a row); the warp copies the
+    // blocks' codes and scales into the tile's slot as soon as that is free.
+    // Block ids are read a tile ahead; a whole cache's rows are asked into L2 a
+    // tile ahead.  (cp.async, not bulk copies: the copy engine takes about 75
+    // cycles for each, and a tile would need 32.)
     int u = part.u0;
     Unit un = load_unit<kSparse>(p, u), nxt{};
     int t_org = part.off0 - part.begin;  // CTA tiles [t_org, t_end) are u's
@@ -670,23 +672,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       else
         ok &= warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort);
     };
-    uint32_t landed[kSlots];  // parity of the last load into a slot
-    int loads = 0;            // slots loaded into (bits)
+    auto publish = [&](const TileMeta& x) {  // the item of the slot, by lane 0
+      if (lane == 0) {
+        meta_s[slot.i] = x;
+        mbar_arrive(&bar_raw[slot.i]);
+      }
+    };
 #pragma unroll 1
     for (int t = 0; t < ntiles; ++t) {
-      const bool scales = lane >= 16;
-      const uint32_t row = scales ? kFp4Groups : kFp4CodeBytes;
-      const uint8_t* src =
-          (scales ? p.scales : p.codes) + (tok0 + (nt > 0 ? pos : 0)) * static_cast<int64_t>(row);
-      if (t > 0 && nt > 0) l2_prefetch(src, nt * row);
       if (m.bits & kFirst) {
         wait_free();
         if (!ok) break;  // uniform
-        if (lane == 0) {
-          meta_s[slot.i].unit = m.unit;
-          meta_s[slot.i].bits = kQueries;
-          mbar_arrive(&bar_raw[slot.i]);
-        }
+        TileMeta x = m;
+        x.bits = kQueries;
+        publish(x);
+        mbar_arrive(&bar_raw[slot.i]);
         slot.next();
       }
       wait_free();
@@ -694,32 +694,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       const uint32_t v = lane < 16 ? ((1u << nt) - 1u) << (4 * (lane & 7)) : 0u;
       m.valid[0] = __reduce_or_sync(0xffffffffu, lane < 8 ? v : 0u);
       m.valid[1] = __reduce_or_sync(0xffffffffu, lane < 8 ? 0u : v);
-      if (lane == 0) {
-        meta_s[slot.i] = m;
-        mbar_arrive_expect_tx(&bar_raw[slot.i], (__popc(m.valid[0]) + __popc(m.valid[1])) *
-                                                    (kFp4CodeBytes + kFp4Groups));
-      }
-      __syncwarp();
-      if (nt > 0) {
-        const int i = lane & 15;
-        const uint32_t dst = slot_u + slot.i * kSlotBytes + (i >> 1) * 1024 +
-                             (scales ? 2 * kRegion + (i & 1) * 64 : (i & 1) * kRegion);
-        bulk_load(dst, src, nt * row, &bar_raw[slot.i]);
+      publish(m);
+      const uint32_t dst = slot_u + slot.i * kSlotBytes;
+      const uint8_t* codes = p.codes + tok0 * kFp4CodeBytes + lane * 16;
+      const int nblk = max(4, ((m.bits & 0xFF) + 15) / 16 * 4);  // a multiple of 16 tokens
+#pragma unroll 4
+      for (int i = 0; i < nblk; ++i) {  // a block's 1 KiB: two copies a lane
+        const int n_i = __shfl_sync(0xffffffffu, nt, i);
+        const int p_i = __shfl_sync(0xffffffffu, pos, i);
+        const int64_t at = n_i > 0 ? p_i : 0;
+        const uint32_t d = dst + (i >> 1) * 1024 + (i & 1) * kRegion + lane * 16;
+        const uint8_t* src = codes + at * kFp4CodeBytes;
+        const bool v0 = (lane >> 4) < n_i, v1 = 2 + (lane >> 4) < n_i;
+        cp_async16(d, v0 ? src : p.codes, v0);
+        cp_async16(d + 512, v1 ? src + 512 : p.codes, v1);
       }
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i)
-        if (i == slot.i) landed[i] = slot.parity;
-      loads |= 1 << slot.i;
+      for (int h = 0; h < 2; ++h) {  // scales: a token's 16 bytes a lane
+        const int i = 8 * h + (lane >> 2), tk = lane & 3;
+        const int n_i = __shfl_sync(0xffffffffu, nt, i), at = __shfl_sync(0xffffffffu, pos, i);
+        cp_async16(dst + (i >> 1) * 1024 + 2 * kRegion + (i & 1) * 64 + tk * 16,
+                   p.scales + (tok0 + (tk < n_i ? at + tk : 0)) * kFp4Groups, tk < n_i);
+      }
+      cp_async_arrive(&bar_raw[slot.i]);
       slot.next();
-      if (t + 1 < ntiles) request(t + 1);
+      if (t + 1 < ntiles) {
+        request(t + 1);
+        if (!kSparse && lane == 0 && (m.bits & 0xFF) > 0) {
+          const int64_t at = tok0 + m.tile * kTT;
+          l2_prefetch(p.codes + at * kFp4CodeBytes, (m.bits & 0xFF) * kFp4CodeBytes);
+          l2_prefetch(p.scales + at * kFp4Groups, (m.bits & 0xFF) * kFp4Groups);
+        }
+      }
     }
     if (lane == 0 && p.comb) p.comb[blockIdx.x] = comb;
-    if (!ok) {  // nothing may land once the block is gone
-      volatile int no_abort = 0;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i)
-        if ((loads >> i) & 1) warp_wait(&bar_raw[i], landed[i], &no_abort);
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands once the block is gone
   } else if (warp < kConvWarp0) {
     // ======================= workers ==========================================
     const int qd = warp & 3, th = warp >> 2, half = lane >> 4;
