@@ -55,8 +55,8 @@ constexpr int kConvWarp0 = 8;    // converter warps 8-15
 constexpr int kConvWarps = 8;
 constexpr int kQkWarp = 16;      // MMA issue
 constexpr int kPvWarp = 17;
-constexpr int kListWarp = 18;    // token lists, loads of codes and scales
-constexpr int kThreads = 19 * 32;  // 96 registers a thread
+constexpr int kListWarp = 18;    // warps 18 and 19: token lists, loads of codes and scales
+constexpr int kThreads = 20 * 32;  // 96 registers a thread
 constexpr int kTT = 64;          // tokens per tile
 constexpr int kM = 64;           // (row, head) pairs per unit (MMA M)
 constexpr int kOct = 8;          // tokens of a tile that a converter warp takes
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bar_raw[i], 33);  // the list warp's lanes, and its description
+      mbar_init(&bar_raw[i], 65);  // the list warps' lanes, and the item's description
       mbar_init(&bar_full[i], kConvWarps);
       mbar_init(&bar_free[i], 1);
     }
@@ -610,14 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       volatile int no_abort = 0;
       warp_wait(&bar_drain, 0, &no_abort);
     }
-  } else if (warp == kListWarp) {
-    // ======================= list warp ========================================
+  } else if (warp >= kListWarp) {
+    // ======================= list warps =======================================
     // Lane i < 16 finds block i of a tile (4 tokens of the list: a selected
-    // block, the partial tail, or four tokens in a row); the warp copies the
+    // block, the partial tail, or four tokens in a row); the warps copy the
     // blocks' codes and scales into the tile's slot as soon as that is free.
     // Block ids are read a tile ahead; a whole cache's rows are asked into L2 a
     // tile ahead.  (cp.async, not bulk copies: the copy engine takes about 75
     // cycles for each, and a tile would need 32.)
+    const int lw = warp - kListWarp;  // even blocks, odd blocks
     int u = part.u0;
     Unit un = load_unit<kSparse>(p, u), nxt{};
     int t_org = part.off0 - part.begin;  // CTA tiles [t_org, t_end) are u's
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         ok &= warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort);
     };
     auto publish = [&](const TileMeta& x) {  // the item of the slot, by lane 0
-      if (lane == 0) {
+      if (lane == 0 && lw == 0) {
         meta_s[slot.i] = x;
         mbar_arrive(&bar_raw[slot.i]);
       }
@@ -699,35 +700,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       const uint8_t* codes = p.codes + tok0 * kFp4CodeBytes + lane * 16;
       const int nblk = max(4, ((m.bits & 0xFF) + 15) / 16 * 4);  // a multiple of 16 tokens
 #pragma unroll 4
-      for (int i = 0; i < nblk; ++i) {  // a block's 1 KiB: two copies a lane
+      for (int i = lw; i < nblk; i += 2) {  // a block's 1 KiB: two copies a lane
         const int n_i = __shfl_sync(0xffffffffu, nt, i);
-        const int p_i = __shfl_sync(0xffffffffu, pos, i);
-        const int64_t at = n_i > 0 ? p_i : 0;
-        const uint32_t d = dst + (i >> 1) * 1024 + (i & 1) * kRegion + lane * 16;
-        const uint8_t* src = codes + at * kFp4CodeBytes;
+        const int at = __shfl_sync(0xffffffffu, pos, i);
+        const uint32_t d = dst + (i >> 1) * 1024 + lw * kRegion + lane * 16;
+        const uint8_t* src = codes + static_cast<int64_t>(at) * kFp4CodeBytes;
         const bool v0 = (lane >> 4) < n_i, v1 = 2 + (lane >> 4) < n_i;
         cp_async16(d, v0 ? src : p.codes, v0);
         cp_async16(d + 512, v1 ? src + 512 : p.codes, v1);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // scales: a token's 16 bytes a lane
-        const int i = 8 * h + (lane >> 2), tk = lane & 3;
+      {  // scales of blocks 8 lw .. 8 lw + 7: a token's 16 bytes a lane
+        const int i = 8 * lw + (lane >> 2), tk = lane & 3;
         const int n_i = __shfl_sync(0xffffffffu, nt, i), at = __shfl_sync(0xffffffffu, pos, i);
         cp_async16(dst + (i >> 1) * 1024 + 2 * kRegion + (i & 1) * 64 + tk * 16,
-                   p.scales + (tok0 + (tk < n_i ? at + tk : 0)) * kFp4Groups, tk < n_i);
+                   p.scales + (tk < n_i ? tok0 + at + tk : 0) * kFp4Groups, tk < n_i);
       }
       cp_async_arrive(&bar_raw[slot.i]);
       slot.next();
       if (t + 1 < ntiles) {
         request(t + 1);
-        if (!kSparse && lane == 0 && (m.bits & 0xFF) > 0) {
+        if (!kSparse && lane == 0 && lw == 1 && (m.bits & 0xFF) > 0) {
           const int64_t at = tok0 + m.tile * kTT;
           l2_prefetch(p.codes + at * kFp4CodeBytes, (m.bits & 0xFF) * kFp4CodeBytes);
           l2_prefetch(p.scales + at * kFp4Groups, (m.bits & 0xFF) * kFp4Groups);
         }
       }
     }
-    if (lane == 0 && p.comb) p.comb[blockIdx.x] = comb;
+    if (lane == 0 && lw == 0 && p.comb) p.comb[blockIdx.x] = comb;
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands once the block is gone
   } else if (warp < kConvWarp0) {
     // ======================= workers ==========================================
