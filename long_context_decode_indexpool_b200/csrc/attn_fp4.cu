@@ -116,32 +116,37 @@ __device__ __forceinline__ void fence_proxy_async() {
 __device__ __forceinline__ void pair_sync(int qd) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
 }
-// A warp's wait for a phase, its threads suspended until the phase completes
-// (or 1 ms has passed: then the abort flag and the limit of 2^32 - 2^28 clocks,
-// about two seconds, are looked at).  On a timeout it sets the abort flag and
-// the error word.  The same result for all lanes.
+// Waits for a phase, suspended until it completes (or 1 ms has passed: then the
+// abort flag and the limit of 2^32 - 2^28 clocks, about two seconds, are looked
+// at).  On a timeout it sets the abort flag and the error word.  Every lane of
+// a warp calls it; the result may differ between lanes only after a timeout.
+__device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(addr), "r"(parity), "r"(1000000)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t addr = smem_u32(bar);
-  const uint32_t t0 = clock();
   bool r = true;
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity), "r"(1000000)
-        : "memory");
-    if (done) break;
-    if (*abort || static_cast<uint32_t>(clock()) - t0 > 0xF0000000u) {
-      if (!*abort) atomicExch(&g_device_error, kErrWaitTimeout);
-      *abort = 1;
-      r = false;
-      break;
+  if (!mbar_try(addr, parity)) {
+    const uint32_t t0 = clock();
+    while (!mbar_try(addr, parity)) {
+      if (*abort || static_cast<uint32_t>(clock()) - t0 > 0xF0000000u) {
+        if (!*abort) atomicExch(&g_device_error, kErrWaitTimeout);
+        *abort = 1;
+        r = false;
+        break;
+      }
     }
   }
-  return __all_sync(0xffffffffu, r);
+  __syncwarp();
+  return r;
 }
 // 16-byte asynchronous copy to shared memory, zeros where `valid` is false; the
 // second makes an mbarrier arrival of the thread's copies so far.
@@ -156,6 +161,36 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Asks `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
 __device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+// Pairs of fp32 values in one register pair (the paired instructions round each
+// as the single ones do).
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return pack2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -412,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   __shared__ uint64_t bar_qk[2], bar_p[2], bar_pv[2];  // S(t), P(t), O of tile t & 1 ready
   __shared__ uint64_t bar_q, bar_drain;                // queries in TMEM; all MMAs done
   __shared__ TileMeta meta_s[kSlots];
-  __shared__ __align__(16) float2 te_s[kSlots][kTT];  // (2^E, E) per token; (1, -inf): nothing there
+  // per token 2^E and E; 1 and -inf where there is nothing
+  __shared__ __align__(16) float tf_s[kSlots][kTT], te_s[kSlots][kTT];
   __shared__ float hs_s[4][kM];                       // per segment, mod 4
   __shared__ float red_m[2][2][kM], red_l[2][kM];
   __shared__ int scratch[kThreads / 32 + 2];
@@ -481,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     // eight different bank groups.
     const uint32_t out_off = (w * kOct + r8) * 128 + (g4 >> 1) * kRegion +
                              (((4 * (g4 & 1)) ^ r8 ^ (g4 & 2)) << 4) + (odd ? 2 * kRegion : 0);
+    const uint32_t odd_back = odd ? 0u - 4 * kRegion : 0u;
     int seg = 0;  // segments begun
 #pragma unroll 1
     for (int t = 0; t < ntiles;) {
@@ -507,13 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // (the raw rows are read)
         // biased exponent of the row, kept where 2^E and 2^-E are normal
         const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
-        if (g4 == 0)
-          te_s[slot.i][w * kOct + r8] =
-              valid ? make_float2(__int_as_float(eb << 23), static_cast<float>(eb - 127))
-                    : make_float2(1.f, -INFINITY);
+        if (g4 == 0) {
+          tf_s[slot.i][w * kOct + r8] = valid ? __int_as_float(eb << 23) : 1.f;
+          te_s[slot.i][w * kOct + r8] = valid ? static_cast<float>(eb - 127) : -INFINITY;
+        }
         // tokens up to the next multiple of 16 take part in the products
         if (w * kOct < max(16, ((bits & 0xFF) + 15) & ~15)) {
           __syncwarp();
+          uint32_t out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = base + (out_off ^ (i << 4));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int b = static_cast<int>(((odd ? sw[k ^ 1] : sw[k]) >> (8 * g4)) & 0xFFu);
@@ -522,15 +562,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
             __half sc = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
             if (b == kFp4NanByte) sc = __ushort_as_half(0x7E00);
             const __half2 s2 = __half2half2(valid ? sc : __ushort_as_half(0));
-            const uint32_t dst = base + (odd ? out_off - 4 * kRegion * (k & 1) : out_off) +
-                                 2 * kRegion * k;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t h[4];
               fp4x8_to_half2x4(swap ? c[k][i ^ 2] : c[k][i], h);
 #pragma unroll
               for (int e = 0; e < 4; ++e) h[e] = h2_bits(__hmul2(*reinterpret_cast<__half2*>(&h[e]), s2));
-              sts128(dst ^ (i << 4), h[0], h[1], h[2], h[3]);
+              sts128(out[i] + (k & 1 ? odd_back : 0) + 2 * kRegion * k, h[0], h[1], h[2], h[3]);
             }
           }
         }
@@ -560,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         // S buffer t & 1 is free once the softmax of tile t-2 has read it
         if (t >= 2) ok &= warp_wait(&bar_p[t & 1], ((t - 2) >> 1) & 1, abort);
         ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
-        if (!ok) break;  // uniform
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         const int bits = meta_s[slot.i].bits;
         fresh = (bits & kLast) != 0;
         tc_fence_after();
@@ -582,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       for (int t = 0; t < ntiles; ++t, slot.next()) {
         if (fresh) slot.next();
         ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
-        if (!ok) break;  // uniform
         const int bits = meta_s[slot.i].bits;
         fresh = (bits & kLast) != 0;
         const int ks = max(1, ((bits & 0xFF) + 15) >> 4);
         ok &= warp_wait(&bar_p[t & 1], (t >> 1) & 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t p_lo = desc_lo(p_u + (t & 1) * kPBytes, 16);
@@ -671,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       if (round < kSlots)
         ++round;
       else
-        ok &= warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort);
+        ok = __all_sync(0xffffffffu, ok && warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort));
     };
     auto publish = [&](const TileMeta& x) {  // the item of the slot, by lane 0
       if (lane == 0 && lw == 0) {
@@ -683,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     for (int t = 0; t < ntiles; ++t) {
       if (m.bits & kFirst) {
         wait_free();
-        if (!ok) break;  // uniform
+        if (!ok) break;
         TileMeta x = m;
         x.bits = kQueries;
         publish(x);
@@ -777,16 +816,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         slot.next();
         continue;
       }
-      const float4* te = reinterpret_cast<const float4*>(&te_s[slot.i][32 * th + 16 * half]);
-      float4 e2[8];  // (2^E, E) of this thread's 16 tokens
+      uint32_t tf[16], te[16];  // 2^E and E of this thread's 16 tokens
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e2[i] = te[i];
+      for (int i = 0; i < 4; ++i) {
+        lds128(smem_u32(&tf_s[slot.i][32 * th + 16 * half + 4 * i]), tf + 4 * i);
+        lds128(smem_u32(&te_s[slot.i][32 * th + 16 * half + 4 * i]), te + 4 * i);
+      }
       slot.next();
       // P buffer t & 1 is free once PV(t-2) is done
       if (t >= 2) ok &= warp_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
       ok &= warp_wait(&bar_qk[buf], (t >> 1) & 1, abort);
       tc_fence_after();
-      float z[16];
+      uint32_t z[16];  // (floats, in pairs for the paired instructions)
       {
         // lanes 0-15 receive the 32 logits of their head in this warp's half
         // of the tile; tokens 16-31 of it go to the partner lane
@@ -796,48 +837,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint32_t v = __shfl_xor_sync(0xffffffffu, a[16 + i], 16);
-          z[i] = __uint_as_float(half ? v : a[i]);
+          z[i] = half ? v : a[i];
         }
       }
-      uint32_t tf[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 e = e2[i];
-        z[2 * i] = fmaf(z[2 * i] * hs, e.x, e.y);
-        z[2 * i + 1] = fmaf(z[2 * i + 1] * hs, e.z, e.w);
-        tf[2 * i] = __float_as_uint(e.x);
-        tf[2 * i + 1] = __float_as_uint(e.z);
+      for (int i = 0; i < 16; i += 2) {
+        const float2 x = unpack2(fma2(mul2(pack2(z[i], z[i + 1]), pack2(hs, hs)),
+                                      pack2(tf[i], tf[i + 1]), pack2(te[i], te[i + 1])));
+        z[i] = __float_as_uint(x.x);
+        z[i + 1] = __float_as_uint(x.y);
       }
       const int lim = min(tm.ntok(), row_lim - tm.tile * kTT) - 32 * th - 16 * half;
       if (__any_sync(0xffffffffu, lim < 16)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = i < lim ? z[i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) z[i] = i < lim ? z[i] : 0xFF800000u;  // -inf
       }
       float mx[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        mx[i] = fmaxf(fmaxf(z[4 * i], z[4 * i + 1]), fmaxf(z[4 * i + 2], z[4 * i + 3]));
+        mx[i] = fmaxf(fmaxf(__uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1])),
+                      fmaxf(__uint_as_float(z[4 * i + 2]), __uint_as_float(z[4 * i + 3])));
       float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
       if (half == 0) red_m[buf][th][m] = mt;
       // The weights, against the running maximum as it stands: most tiles leave
       // it, so the exchange with the other warp of the pair ends behind them.
       uint32_t packed[8];
-      float ls[4], alpha = 1.f;
+      float alpha = 1.f, lsum;
       auto weights = [&] {
         const float ref = m_run == -INFINITY ? 0.f : m_run - kLift;
+        const uint64_t nref = pack2(-ref, -ref);
+        uint64_t ls = 0;  // (0, 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float e[4];
-          ls[i] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[k] = ex2(z[4 * i + k] - ref);
-            ls[i] = fmaf(e[k], __uint_as_float(0x7F000000u - tf[4 * i + k]), ls[i]);  // times 2^-E
-          }
-          packed[2 * i] = h2_bits(__floats2half2_rn(e[0], e[1]));
-          packed[2 * i + 1] = h2_bits(__floats2half2_rn(e[2], e[3]));
+        for (int i = 0; i < 16; i += 2) {
+          const float2 d = unpack2(add2(pack2(z[i], z[i + 1]), nref));
+          const float2 e = make_float2(ex2(d.x), ex2(d.y));
+          // times 2^-E, the bits of which are those of 2^E mirrored
+          ls = fma2(pack2(e.x, e.y), pack2(0x7F000000u - tf[i], 0x7F000000u - tf[i + 1]), ls);
+          packed[i / 2] = h2_bits(__floats2half2_rn(e.x, e.y));
         }
+        const float2 l2 = unpack2(ls);
+        lsum = l2.x + l2.y;
       };
       weights();
       pair_sync(qd);
@@ -869,7 +909,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         }
         weights();
       }
-      float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
       lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
       l_run = fmaf(l_run, alpha, lsum);  // this warp's half of the tokens
 #pragma unroll
