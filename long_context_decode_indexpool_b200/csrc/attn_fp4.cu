@@ -979,73 +979,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the units that several CTAs shared: block (c, y) the unit
-// whose first part CTA c left, pieces 2y and 2y + 1 of 64 (four dims in each of
-// a pair's two halves).
+// Joins the parts of the units that several CTAs shared.  Block (c, y) takes the
+// unit whose first part CTA c left and an equal share of its pieces of 4 dims;
+// a thread a piece, in one pass over the parts with a running R (a part's loads
+// then wait for nothing but the unit's record).  With few units the shares are
+// small (many blocks, many loads in flight), with many they are larger (fewer
+// blocks that find nothing to do).
+constexpr int kJoinThreads = 256;
 template <bool kSparse>
-__global__ void __launch_bounds__(kWork) k_attn_fp4_combine(const KParams p) {
-  __shared__ float w_s[kMaxGrid][kM];
-  __shared__ float inv_s[kM];
+__global__ void __launch_bounds__(kJoinThreads) k_attn_fp4_combine(const KParams p) {
   pdl_wait();
-  const int c = blockIdx.x, piece = blockIdx.y, tid = threadIdx.x;
+  const int c = blockIdx.x, tid = threadIdx.x;
   const int2 cb = p.comb[c];
   const int parts = cb.y;
   if (parts == 0) return;
-  auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
-  // weights 2^(R_i - R) of the parts and 1 / l of each pair: 4 threads a pair
-  {
-    const int m = tid >> 2, j = tid & 3;
-    float R = -INFINITY;
-    for (int i = j; i < parts; i += 4) {
-      const float2 ml = p.part_ml[slot(i) * kM + m];
-      w_s[i][m] = ml.x;
-      R = fmaxf(R, ml.x);
-    }
-    R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, 1));
-    R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, 2));
-    float l = 0.f;
-    for (int i = j; i < parts; i += 4) {
-      const float Ri = w_s[i][m];
-      const float w = Ri == -INFINITY ? (R == -INFINITY ? 1.f : 0.f) : ex2(Ri - R);
-      w_s[i][m] = w;
-      l = fmaf(w, p.part_ml[slot(i) * kM + m].y, l);
-    }
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (j == 0) {
-      inv_s[m] = l != 0.f ? 1.f / l : 0.f;
-      if (piece == 0 && p.lse) {
-        const UnitRows ur = unit_rows<kSparse>(p, cb.x);
-        const int hpr = min(p.heads, kM), rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
-        if (rr < ur.nrows && h < p.heads)
-          p.lse[static_cast<int64_t>(ur.row0 + rr) * p.heads + h] =
-              l != 0.f ? (R + log2f(l)) * 0.69314718055994530942f : -INFINITY;
-      }
-    }
-  }
-  __syncthreads();
-  const int wt = tid & 127, piece4 = 2 * piece + (tid >> 7);
-  const int qd = (wt >> 4) & 3, th = wt >> 6, m = qd * 16 + (wt & 15);
+  const int wt = tid & 127, th = wt >> 6, m = wt & 63;  // part_o's order: half of the dims, pair
   const UnitRows ur = unit_rows<kSparse>(p, cb.x);
   const int hpr = min(p.heads, kM), rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
   if (rr >= ur.nrows || h >= p.heads) return;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* src = p.part_o + piece4 * (kWork / 2) + wt;
+  const int64_t row = static_cast<int64_t>(ur.row0 + rr) * p.heads + h;
+  const int share = 64 / static_cast<int>(gridDim.y);  // pieces of each half
+#pragma unroll 1
+  for (int k = tid >> 7; k < share; k += kJoinThreads / 128) {
+    const int piece = static_cast<int>(blockIdx.y) * share + k;
+    const float4* src = p.part_o + piece * (kWork / 2) + wt;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float R = -INFINITY, l = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float4 v = src[static_cast<int64_t>(slot(i)) * (kPartFloats / 4)];
-    const float w = w_s[i][m];
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+    for (int i = 0; i < parts; ++i) {
+      // slot of part i: CTA c's second, then the first of the CTAs behind it
+      const int slot = 2 * (c + i) + (i == 0 ? 1 : 0);
+      const float4 x = src[static_cast<int64_t>(slot) * (kPartFloats / 4)];
+      const float2 ml = p.part_ml[slot * kM + m];
+      const float top = fmaxf(R, ml.x);
+      // (a part that saw nothing has R = -inf and zeros)
+      const float old = R == -INFINITY ? 0.f : ex2(R - top);
+      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - top);
+      R = top;
+      l = fmaf(w, ml.y, l * old);
+      a.x = fmaf(w, x.x, a.x * old);
+      a.y = fmaf(w, x.y, a.y * old);
+      a.z = fmaf(w, x.z, a.z * old);
+      a.w = fmaf(w, x.w, a.w * old);
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv),
+                                 __floats2bfloat162_rn(a.z * inv, a.w * inv)};
+    *reinterpret_cast<uint2*>(p.out + row * kLatent + 256 * th + 4 * piece) =
+        *reinterpret_cast<const uint2*>(o);
+    if (piece == 0 && th == 0 && p.lse)
+      p.lse[row] = l != 0.f ? (R + log2f(l)) * 0.69314718055994530942f : -INFINITY;
   }
-  const float inv = inv_s[m];
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(ur.row0 + rr) * p.heads + h) * kLatent +
-                            256 * th + 4 * piece4) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 template <bool kSparse>
@@ -1069,7 +1053,8 @@ cudaError_t launch(const AttnFp4Plan& pl, const KParams& p, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (pl.ws_bytes > 0) {
-    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, 32), dim3(kWork), 0, stream,
+    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, pl.units < 32 ? 32 : 8),
+                  dim3(kJoinThreads), 0, stream,
                   true, 1, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
