@@ -130,7 +130,10 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        # the handle alone: torch.cuda.current_stream() also builds a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

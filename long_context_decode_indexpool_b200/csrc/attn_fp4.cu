@@ -69,6 +69,7 @@ constexpr int kSmemBytes = 1024 + kSlots * kSlotBytes + 2 * kPBytes;
 // TMEM columns: in lanes 0-15 of each quarter the queries (two fp16 values a
 // column) and the logits, in lanes 16-31 the output
 constexpr int kColS = 256;
+constexpr int kNear = 4;        // exponents of 8 rows that share one reference, at most apart
 constexpr float kLazy = 8.f;   // the maximum is raised when exceeded by more
 constexpr float kLift = 7.f;   // P = 2^(z - max + 7)
 constexpr int kMaxGrid = 160;  // CTAs (one per SM, at most)
@@ -447,7 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   __shared__ uint64_t bar_qk[2], bar_p[2], bar_pv[2];  // S(t), P(t), O of tile t & 1 ready
   __shared__ uint64_t bar_q, bar_drain;                // queries in TMEM; all MMAs done
   __shared__ TileMeta meta_s[kSlots];
-  // per token 2^E and E; 1 and -inf where there is nothing
+  // 2^E and E of each group of 8 tokens, or (0, inf): its tokens have their own,
+  // in tf_s and te_s
+  __shared__ __align__(16) float2 oct_s[kSlots][kConvWarps];
   __shared__ __align__(16) float tf_s[kSlots][kTT], te_s[kSlots][kTT];
   __shared__ float hs_s[4][kM];                       // per segment, mod 4
   __shared__ float red_m[2][2][kM], red_l[2][kM];
@@ -544,10 +547,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // (the raw rows are read)
         // biased exponent of the row, kept where 2^E and 2^-E are normal
         const int eb = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16)) - 1, 1), 253);
-        if (g4 == 0) {
-          tf_s[slot.i][w * kOct + r8] = valid ? __int_as_float(eb << 23) : 1.f;
-          te_s[slot.i][w * kOct + r8] = valid ? static_cast<float>(eb - 127) : -INFINITY;
+        // The 8 rows share the largest of their exponents where none is further
+        // than 4 below it (they are then still exact: 2^-1 2^-15 2^-4 is above
+        // fp16's last bit, and P loses at most 4 of its 31 bits below the
+        // largest term); otherwise each row has its own.
+        const int top = __reduce_max_sync(0xffffffffu, valid ? eb : 1);
+        const bool wide = top - __reduce_min_sync(0xffffffffu, valid ? eb : top) > kNear;
+        const int ref = wide ? eb : top;
+        if (wide && g4 == 0) {
+          tf_s[slot.i][w * kOct + r8] = __int_as_float(ref << 23);
+          te_s[slot.i][w * kOct + r8] = static_cast<float>(ref - 127);
         }
+        if (lane == 0)
+          oct_s[slot.i][w] = wide ? make_float2(0.f, INFINITY)
+                                  : make_float2(__int_as_float(ref << 23), static_cast<float>(ref - 127));
         // tokens up to the next multiple of 16 take part in the products
         if (w * kOct < max(16, ((bits & 0xFF) + 15) & ~15)) {
           __syncwarp();
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
             const int b = static_cast<int>(((odd ? sw[k ^ 1] : sw[k]) >> (8 * g4)) & 0xFFu);
             // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group; 0 where
             // there is no token)
-            __half sc = __float2half_rn(__int_as_float(max(127 + b - eb, 97) << 23));
+            __half sc = __float2half_rn(__int_as_float(max(127 + b - ref, 97) << 23));
             if (b == kFp4NanByte) sc = __ushort_as_half(0x7E00);
             const __half2 s2 = __half2half2(valid ? sc : __ushort_as_half(0));
 #pragma unroll
@@ -816,12 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         slot.next();
         continue;
       }
-      uint32_t tf[16], te[16];  // 2^E and E of this thread's 16 tokens
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lds128(smem_u32(&tf_s[slot.i][32 * th + 16 * half + 4 * i]), tf + 4 * i);
-        lds128(smem_u32(&te_s[slot.i][32 * th + 16 * half + 4 * i]), te + 4 * i);
-      }
+      // (2^E, E) of this thread's two groups of 8 tokens
+      uint32_t oc[4];
+      lds128(smem_u32(&oct_s[slot.i][4 * th + 2 * half]), oc);
+      const bool own = __any_sync(0xffffffffu, oc[1] == 0x7F800000u || oc[3] == 0x7F800000u);
+      const uint32_t tf_u = smem_u32(&tf_s[slot.i][32 * th + 16 * half]),
+                     te_u = smem_u32(&te_s[slot.i][32 * th + 16 * half]);
       slot.next();
       // P buffer t & 1 is free once PV(t-2) is done
       if (t >= 2) ok &= warp_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
@@ -840,17 +853,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           z[i] = half ? v : a[i];
         }
       }
+      auto factors = [&](int i, uint32_t* f, uint32_t* e) {  // of tokens i .. i + 3
+        f[0] = f[1] = f[2] = f[3] = oc[i < 8 ? 0 : 2];
+        e[0] = e[1] = e[2] = e[3] = oc[i < 8 ? 1 : 3];
+        if (e[0] == 0x7F800000u) {
+          lds128(tf_u + 4 * i, f);
+          lds128(te_u + 4 * i, e);
+        }
+      };
+      if (!own) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float2 x = unpack2(fma2(mul2(pack2(z[i], z[i + 1]), pack2(hs, hs)),
-                                      pack2(tf[i], tf[i + 1]), pack2(te[i], te[i + 1])));
-        z[i] = __float_as_uint(x.x);
-        z[i + 1] = __float_as_uint(x.y);
+        for (int g = 0; g < 2; ++g) {
+          const float f = __uint_as_float(oc[2 * g]) * hs, e = __uint_as_float(oc[2 * g + 1]);
+#pragma unroll
+          for (int i = 8 * g; i < 8 * g + 8; i += 2) {
+            const float2 x = unpack2(fma2(pack2(z[i], z[i + 1]), pack2(f, f), pack2(e, e)));
+            z[i] = __float_as_uint(x.x);
+            z[i + 1] = __float_as_uint(x.y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          uint32_t f[4], e[4];
+          factors(i, f, e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            z[i + k] = __float_as_uint(fmaf(__uint_as_float(z[i + k]) * hs, __uint_as_float(f[k]),
+                                            __uint_as_float(e[k])));
+        }
       }
-      const int lim = min(tm.ntok(), row_lim - tm.tile * kTT) - 32 * th - 16 * half;
-      if (__any_sync(0xffffffffu, lim < 16)) {
+      {
+        const int lim = row_lim - tm.tile * kTT - 32 * th - 16 * half;
+        uint32_t sees = (tm.valid[th] >> (16 * half)) & 0xFFFFu;
+        if (lim < 16) sees &= (1u << max(lim, 0)) - 1u;
+        if (__any_sync(0xffffffffu, sees != 0xFFFFu)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = i < lim ? z[i] : 0xFF800000u;  // -inf
+          for (int i = 0; i < 16; ++i) z[i] = (sees >> i) & 1u ? z[i] : 0xFF800000u;  // -inf
+        }
       }
       float mx[4];
 #pragma unroll
@@ -866,18 +906,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       float alpha = 1.f, lsum;
       auto weights = [&] {
         const float ref = m_run == -INFINITY ? 0.f : m_run - kLift;
-        const uint64_t nref = pack2(-ref, -ref);
-        uint64_t ls = 0;  // (0, 0)
+        lsum = 0.f;  // each weight times 2^-E, the bits of which are those of 2^E mirrored
+        if (!own) {
+          const uint64_t nref = pack2(-ref, -ref);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 d = unpack2(add2(pack2(z[i], z[i + 1]), nref));
-          const float2 e = make_float2(ex2(d.x), ex2(d.y));
-          // times 2^-E, the bits of which are those of 2^E mirrored
-          ls = fma2(pack2(e.x, e.y), pack2(0x7F000000u - tf[i], 0x7F000000u - tf[i + 1]), ls);
-          packed[i / 2] = h2_bits(__floats2half2_rn(e.x, e.y));
+          for (int g = 0; g < 2; ++g) {
+            uint64_t ls = 0;  // (0, 0)
+#pragma unroll
+            for (int i = 8 * g; i < 8 * g + 8; i += 2) {
+              const float2 d = unpack2(add2(pack2(z[i], z[i + 1]), nref));
+              const float2 e = make_float2(ex2(d.x), ex2(d.y));
+              packed[i / 2] = h2_bits(__floats2half2_rn(e.x, e.y));
+              ls = add2(ls, pack2(e.x, e.y));
+            }
+            const float2 l2 = unpack2(ls);
+            lsum = fmaf(l2.x + l2.y, __uint_as_float(0x7F000000u - oc[2 * g]), lsum);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            uint32_t f[4], e[4];
+            factors(i, f, e);
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = ex2(__uint_as_float(z[i + k]) - ref);
+              lsum = fmaf(x[k], __uint_as_float(0x7F000000u - f[k]), lsum);
+            }
+            packed[i / 2] = h2_bits(__floats2half2_rn(x[0], x[1]));
+            packed[i / 2 + 1] = h2_bits(__floats2half2_rn(x[2], x[3]));
+          }
         }
-        const float2 l2 = unpack2(ls);
-        lsum = l2.x + l2.y;
       };
       weights();
       pair_sync(qd);
@@ -938,19 +997,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       float4* part = p.part_o + static_cast<int64_t>(part_slot) * (kPartFloats / 4) + 16 * warp +
                      (lane & 15);
 #pragma unroll 1
-      for (int c0 = 0; c0 < 256; c0 += 32) {
-        float v[32];
-        tmem_ld_32x32b_x32(tm_q + 256 * th + c0, v);
+      for (int c0 = 0; c0 < 256; c0 += 64) {
+        uint32_t raw[64];
+        tmem_ld_x32_async(tm_q + 256 * th + c0, raw);
+        tmem_ld_x32_async(tm_q + 256 * th + c0 + 32, raw + 32);
+        tmem_ld_wait_regs<64>(raw);
         if (half == 0) continue;
+        const float* v = reinterpret_cast<const float*>(raw);
         if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 16; ++i)
             part[(c0 / 4 + i) * (kWork / 2)] =
                 make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else if (out_row >= 0) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kLatent + 256 * th + c0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 8; ++i) {
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
