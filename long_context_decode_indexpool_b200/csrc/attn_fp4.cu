@@ -105,7 +105,6 @@ struct __align__(16) TileMeta {
   int tile;           // index in the unit
   int bits;           // tokens in its part of the list (0..64), and flags
   uint32_t valid[2];  // a bit per token that has a row in the cache
-  __device__ int ntok() const { return bits & 0xFF; }
 };
 // first, last tile of its segment; the segment has the unit's first, last tile;
 // not a tile but its segment's queries
@@ -114,7 +113,11 @@ enum : int { kFirst = 256, kLast = 512, kHead = 1024, kTail = 2048, kQueries = 4
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// Barrier of the two worker warps that share TMEM lane quarter qd (ids 1-4).
+// (Instructions with .aligned want the warp converged: every divergent piece
+// of code before one ends with a __syncwarp.)
 __device__ __forceinline__ void pair_sync(int qd) {
+  __syncwarp();
   asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
 }
 // Waits for a phase, suspended until it completes (or 1 ms has passed: then the
@@ -181,11 +184,6 @@ __device__ __forceinline__ float2 unpack2(uint64_t x) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -476,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     fence_mbar_init();
   }
   if (warp == 0) {
+    __syncwarp();
     tmem_alloc(&tmem_holder, 512);
     tmem_relinquish();
   }
@@ -999,6 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll 1
       for (int c0 = 0; c0 < 256; c0 += 64) {
         uint32_t raw[64];
+        __syncwarp();
         tmem_ld_x32_async(tm_q + 256 * th + c0, raw);
         tmem_ld_x32_async(tm_q + 256 * th + c0 + 32, raw + 32);
         tmem_ld_wait_regs<64>(raw);
