@@ -382,33 +382,42 @@ __device__ __forceinline__ Part plan_part(const KParams& p, int* scratch /* [kTh
 }
 
 // ---- queries ------------------------------------------------------------------
+// The row of a (row, head) pair within its unit; hpr heads a row, 16 at least.
+__device__ __forceinline__ int pair_row(int m, int hpr) {
+  return (m >= hpr ? 1 : 0) + (m >= 2 * hpr ? 1 : 0) + (m >= 3 * hpr ? 1 : 0);
+}
+
 // Rows w, w + 8, .. of the unit's 64 query rows to a shared-memory slot as
 // fp16, each scaled by a power of two; hs[m] is what a product with it is
-// multiplied by.
+// multiplied by.  (Two rows at a time in a rolled loop: it runs once a segment,
+// and unrolled over eight rows its instruction fetches took longer than its
+// loads.)
 template <bool kSparse>
 __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t slot, float* hs, int w) {
-  constexpr int nw = kConvWarps;
   const int lane = threadIdx.x & 31;
   const UnitRows r = unit_rows<kSparse>(p, u);
   const int hpr = min(p.heads, kM);  // heads of a row in the unit
-#pragma unroll 1
-  for (int m0 = w; m0 < kM; m0 += 4 * nw) {
-    uint4 v[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + i * nw;
-      const int rr = m / hpr, h = r.hg * kM + m - rr * hpr;
-      v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < r.nrows && h < p.heads) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (static_cast<int64_t>(r.row0 + rr) * p.heads + h) * kLatent);
-        v[i][0] = src[lane];
-        v[i][1] = src[32 + lane];
-      }
+  const uint4* src = reinterpret_cast<const uint4*>(
+      p.q + (static_cast<int64_t>(r.row0) * p.heads + r.hg * kM) * kLatent);
+  // pairs past this one are padding (rows of a unit follow each other in q)
+  const int pairs = min(r.nrows * hpr, p.heads * r.nrows - r.hg * kM);
+  auto fetch = [&](int m, uint4* v) {
+    v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (m < pairs) {
+      v[0] = src[m * 64 + lane];
+      v[1] = src[m * 64 + 32 + lane];
     }
+  };
+  uint4 v[2][2], nx[2][2];
+  fetch(w, v[0]);
+  fetch(w + kConvWarps, v[1]);
+#pragma unroll 1
+  for (int m0 = w; m0 < kM; m0 += 2 * kConvWarps) {
+    fetch(m0 + 2 * kConvWarps, nx[0]);
+    fetch(m0 + 3 * kConvWarps, nx[1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + i * nw;
+    for (int i = 0; i < 2; ++i) {
+      const int m = m0 + i * kConvWarps;
       const uint32_t mask = 0x7FFF7FFFu;
       uint32_t a = __vmaxu2(__vmaxu2(v[i][0].x & mask, v[i][0].y & mask),
                             __vmaxu2(v[i][0].z & mask, v[i][0].w & mask));
@@ -431,6 +440,11 @@ __device__ __forceinline__ void load_q(const KParams& p, int u, uint32_t slot, f
                o[2], o[3]);
       }
       if (lane == 0) hs[m] = p.scale_log2 * __int_as_float((127 - s) << 23);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[i][0] = nx[i][0];
+      v[i][1] = nx[i][1];
     }
   }
 }
@@ -682,6 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       const int row0 = unit_rows<kSparse>(p, u).row0;
       tok0 = static_cast<int64_t>(kSparse ? row0 : row0 / p.per_seq) * p.seq_tok;
       ids = p.idx + static_cast<int64_t>(row0) * kTopK;  // (unused when dense)
+      if (lane == 0 && lw == 1 && t_end < ntiles) {  // the next unit's queries, into L2
+        const UnitRows r = unit_rows<kSparse>(p, u + 1);
+        l2_prefetch(p.q + (static_cast<int64_t>(r.row0) * p.heads + r.hg * kM) * kLatent,
+                    min(r.nrows * min(p.heads, kM), p.heads * r.nrows - r.hg * kM) * kLatent * 2);
+      }
       if (t_org >= 0 && t_end > ntiles)  // the split unit that begins here
         comb = make_int2(u, (part.begin + t_end - 1) / part.quota - static_cast<int>(blockIdx.x) + 1);
     };
@@ -800,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         m_run = -INFINITY;
         l_run = 0.f;
         const UnitRows ur = unit_rows<kSparse>(p, tm.unit);
-        const int rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
+        const int rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
         const bool mine = rr < ur.nrows && h < p.heads;
         out_row = mine ? static_cast<int64_t>(ur.row0 + rr) * p.heads + h : -1;
         // rows of one unit may see different numbers of tokens
@@ -1057,7 +1076,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_fp4_combine(const KParams
   if (parts == 0) return;
   const int wt = tid & 127, th = wt >> 6, m = wt & 63;  // part_o's order: half of the dims, pair
   const UnitRows ur = unit_rows<kSparse>(p, cb.x);
-  const int hpr = min(p.heads, kM), rr = m / hpr, h = ur.hg * kM + m - rr * hpr;
+  const int hpr = min(p.heads, kM), rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
   if (rr >= ur.nrows || h >= p.heads) return;
   const int64_t row = static_cast<int64_t>(ur.row0 + rr) * p.heads + h;
   const int share = 64 / static_cast<int>(gridDim.y);  // pieces of each half
