@@ -1021,15 +1021,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         tmem_ld_x32_async(tm_q + 256 * th + c0, raw);
         tmem_ld_x32_async(tm_q + 256 * th + c0 + 32, raw + 32);
         tmem_ld_wait_regs<64>(raw);
-        if (half == 0) continue;
         const float* v = reinterpret_cast<const float*>(raw);
         if (!whole) {
+          if (half == 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            part[(c0 / 4 + i) * (kWork / 2)] =
-                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else if (out_row >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kLatent + 256 * th + c0);
+            for (int i = 0; i < 16; ++i)
+              part[(c0 / 4 + i) * (kWork / 2)] =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          continue;
+        }
+        // 16 rows of 64 dims through 2 KiB of the P buffers (idle until every
+        // worker has passed the next segment's queries), so that eight lanes
+        // store a row's 128 bytes: stores straight from the lanes of TMEM's
+        // rows took 5,500 cycles a segment.
+        const uint32_t stage = p_u + warp * 2048;
+        if (half == 1) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t o[4];
@@ -1039,8 +1046,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
                   __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
               o[k] = *reinterpret_cast<const uint32_t*>(&h2);
             }
-            dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            sts128(stage + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
           }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const int64_t row = __shfl_sync(0xffffffffu, out_row, r);
+          uint32_t o[4];
+          lds128(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4), o);
+          if (row >= 0)
+            *reinterpret_cast<uint4*>(p.out + row * kLatent + 256 * th + c0 + 8 * (lane & 7)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       if (half == 0 && th == 0) {
