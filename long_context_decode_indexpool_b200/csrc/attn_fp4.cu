@@ -73,7 +73,7 @@ constexpr int kNear = 4;        // exponents of 8 rows that share one reference,
 constexpr float kLazy = 8.f;   // the maximum is raised when exceeded by more
 constexpr float kLift = 7.f;   // P = 2^(z - max + 7)
 constexpr int kMaxGrid = 160;  // CTAs (one per SM, at most)
-constexpr int kPartFloats = kM * kLatent;
+constexpr int kPartHalfs = kM * kLatent;
 constexpr uint32_t kIdescF16 = (1u << 4) | (static_cast<uint32_t>(kM >> 4) << 24);  // f16 A, B; f32 D
 constexpr uint32_t kIdescPV = kIdescF16 | ((256u >> 3) << 17) | (1u << 16);  // B MN-major
 static_assert(kSmemBytes + 6 * 1024 <= 232448, "shared memory budget");
@@ -95,8 +95,8 @@ struct KParams {
   __nv_bfloat16* out;
   float* lse;
   int2* comb;      // [grid] (unit, CTAs it spans) of the split unit that begins in a CTA
-  float2* part_ml; // [2 grid][64] (R, l)
-  float4* part_o;  // [2 grid][64 pieces of 4 dims][8 worker warps][16 pairs]
+  float4* part_ml; // [2 grid][64] (R, l, sum of the weights)
+  __half* part_o;  // [2 grid][64][512] O / sum of the weights
 };
 
 // A tile as the list warp describes it to the other roles.
@@ -465,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   __shared__ __align__(16) float2 oct_s[kSlots][kConvWarps];
   __shared__ __align__(16) float tf_s[kSlots][kTT], te_s[kSlots][kTT];
   __shared__ float hs_s[4][kM];                       // per segment, mod 4
-  __shared__ float red_m[2][2][kM], red_l[2][kM];
+  __shared__ float red_m[2][2][kM];
+  __shared__ float2 red_l[2][kM];
   __shared__ int scratch[kThreads / 32 + 2];
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_s;
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     const int hpr = min(p.heads, kM);
     int seg = 0, row_lim = 0;
     int64_t out_row = -1;  // row of out of this thread, or -1
-    float hs = 0.f, m_run = -INFINITY, l_run = 0.f;
+    float hs = 0.f, m_run = -INFINITY, l_run = 0.f, w_run = 0.f;  // w_run: sum of the weights
 #pragma unroll 1
     for (int t = 0; t < ntiles;) {
       const int buf = t & 1;
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         hs = hs_s[seg & 3][m];
         ++seg;
         m_run = -INFINITY;
-        l_run = 0.f;
+        l_run = w_run = 0.f;
         const UnitRows ur = unit_rows<kSparse>(p, tm.unit);
         const int rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
         const bool mine = rr < ur.nrows && h < p.heads;
@@ -921,10 +922,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       // The weights, against the running maximum as it stands: most tiles leave
       // it, so the exchange with the other warp of the pair ends behind them.
       uint32_t packed[8];
-      float alpha = 1.f, lsum;
+      float alpha = 1.f, lsum, wsum;
       auto weights = [&] {
         const float ref = m_run == -INFINITY ? 0.f : m_run - kLift;
-        lsum = 0.f;  // each weight times 2^-E, the bits of which are those of 2^E mirrored
+        lsum = wsum = 0.f;  // lsum: times 2^-E, the bits of which are those of 2^E mirrored
         if (!own) {
           const uint64_t nref = pack2(-ref, -ref);
 #pragma unroll
@@ -938,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
               ls = add2(ls, pack2(e.x, e.y));
             }
             const float2 l2 = unpack2(ls);
+            wsum += l2.x + l2.y;
             lsum = fmaf(l2.x + l2.y, __uint_as_float(0x7F000000u - oc[2 * g]), lsum);
           }
         } else {
@@ -949,6 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               x[k] = ex2(__uint_as_float(z[i + k]) - ref);
+              wsum += x[k];
               lsum = fmaf(x[k], __uint_as_float(0x7F000000u - f[k]), lsum);
             }
             packed[i / 2] = h2_bits(__floats2half2_rn(x[0], x[1]));
@@ -988,6 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       }
       lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
       l_run = fmaf(l_run, alpha, lsum);  // this warp's half of the tokens
+      w_run = fmaf(w_run, alpha, wsum);  // (and this lane's: joined at the end)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int piece = 4 * th + 2 * half + c;
@@ -1003,17 +1007,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       if (!(tm.bits & kLast)) continue;
 
       // ---- the segment's output (in lanes 16-31; a warp has 256 dims) --------
-      if (half == 0) red_l[th][m] = l_run;
+      w_run += __shfl_xor_sync(0xffffffffu, w_run, 16);
+      if (half == 0) red_l[th][m] = make_float2(l_run, w_run);
       pair_sync(qd);
-      l_run += red_l[th ^ 1][m];
+      l_run += red_l[th ^ 1][m].x;
+      w_run += red_l[th ^ 1][m].y;
       ok &= warp_wait(&bar_pv[buf], pv_parity, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
       const bool whole = (tm.bits & (kHead | kTail)) == (kHead | kTail);
-      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      // A whole unit: out = O / l in bf16.  A part: O / (sum of its weights), at
+      // most 24 in magnitude, in fp16 (11 bits: a fifth of the output's own
+      // rounding when joined; fp32 parts took twice the traffic).
+      const float norm = whole ? l_run : w_run, inv = norm != 0.f ? 1.f / norm : 0.f;
       const int part_slot = 2 * blockIdx.x + ((tm.bits & kHead) ? 1 : 0);
-      float4* part = p.part_o + static_cast<int64_t>(part_slot) * (kPartFloats / 4) + 16 * warp +
-                     (lane & 15);
+      const int64_t dst_row = whole ? out_row : static_cast<int64_t>(part_slot) * kM + m;
+      uint16_t* const dst =
+          whole ? reinterpret_cast<uint16_t*>(p.out) : reinterpret_cast<uint16_t*>(p.part_o);
 #pragma unroll 1
       for (int c0 = 0; c0 < 256; c0 += 64) {
         uint32_t raw[64];
@@ -1022,15 +1032,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         tmem_ld_x32_async(tm_q + 256 * th + c0 + 32, raw + 32);
         tmem_ld_wait_regs<64>(raw);
         const float* v = reinterpret_cast<const float*>(raw);
-        if (!whole) {
-          if (half == 1) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              part[(c0 / 4 + i) * (kWork / 2)] =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-          continue;
-        }
         // 16 rows of 64 dims through 2 KiB of the P buffers (idle until every
         // worker has passed the next segment's queries), so that eight lanes
         // store a row's 128 bytes: stores straight from the lanes of TMEM's
@@ -1042,9 +1043,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 h2 =
-                  __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
-              o[k] = *reinterpret_cast<const uint32_t*>(&h2);
+              const float a = v[8 * i + 2 * k] * inv, b = v[8 * i + 2 * k + 1] * inv;
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+              o[k] = whole ? *reinterpret_cast<const uint32_t*>(&h2)
+                           : h2_bits(__floats2half2_rn(a, b));
             }
             sts128(stage + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
           }
@@ -1053,17 +1055,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * i + (lane >> 3);
-          const int64_t row = __shfl_sync(0xffffffffu, out_row, r);
+          const int64_t row = __shfl_sync(0xffffffffu, dst_row, r);
           uint32_t o[4];
           lds128(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4), o);
           if (row >= 0)
-            *reinterpret_cast<uint4*>(p.out + row * kLatent + 256 * th + c0 + 8 * (lane & 7)) =
+            *reinterpret_cast<uint4*>(dst + row * kLatent + 256 * th + c0 + 8 * (lane & 7)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       if (half == 0 && th == 0) {
         if (!whole)
-          p.part_ml[part_slot * kM + m] = make_float2(ref_out, l_run);
+          p.part_ml[part_slot * kM + m] = make_float4(ref_out, l_run, w_run, 0.f);
         else if (p.lse && out_row >= 0)
           p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
                                         : -INFINITY;
@@ -1079,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 }
 
 // Joins the parts of the units that several CTAs shared.  Block (c, y) takes the
-// unit whose first part CTA c left and an equal share of its pieces of 4 dims;
+// unit whose first part CTA c left and an equal share of its pieces of 8 dims;
 // a thread a piece, in one pass over the parts with a running R (a part's loads
 // then wait for nothing but the unit's record).  With few units the shares are
 // small (many blocks, many loads in flight), with many they are larger (fewer
@@ -1092,41 +1094,46 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_fp4_combine(const KParams
   const int2 cb = p.comb[c];
   const int parts = cb.y;
   if (parts == 0) return;
-  const int wt = tid & 127, th = wt >> 6, m = wt & 63;  // part_o's order: half of the dims, pair
   const UnitRows ur = unit_rows<kSparse>(p, cb.x);
-  const int hpr = min(p.heads, kM), rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
-  if (rr >= ur.nrows || h >= p.heads) return;
-  const int64_t row = static_cast<int64_t>(ur.row0 + rr) * p.heads + h;
-  const int share = 64 / static_cast<int>(gridDim.y);  // pieces of each half
+  const int hpr = min(p.heads, kM);
+  const int pairs = kM / static_cast<int>(gridDim.y);
 #pragma unroll 1
-  for (int k = tid >> 7; k < share; k += kJoinThreads / 128) {
-    const int piece = static_cast<int>(blockIdx.y) * share + k;
-    const float4* src = p.part_o + piece * (kWork / 2) + wt;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = tid >> 6; k < pairs; k += kJoinThreads / 64) {
+    const int m = static_cast<int>(blockIdx.y) * pairs + k, d = 8 * (tid & 63);
+    const int rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
+    if (rr >= ur.nrows || h >= p.heads) continue;
+    const int64_t row = static_cast<int64_t>(ur.row0 + rr) * p.heads + h;
+    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     float R = -INFINITY, l = 0.f;
 #pragma unroll 8
     for (int i = 0; i < parts; ++i) {
       // slot of part i: CTA c's second, then the first of the CTAs behind it
-      const int slot = 2 * (c + i) + (i == 0 ? 1 : 0);
-      const float4 x = src[static_cast<int64_t>(slot) * (kPartFloats / 4)];
-      const float2 ml = p.part_ml[slot * kM + m];
+      const int slot = (2 * (c + i) + (i == 0 ? 1 : 0)) * kM + m;
+      const uint4 x = *reinterpret_cast<const uint4*>(p.part_o + static_cast<int64_t>(slot) * kLatent + d);
+      const float4 ml = p.part_ml[slot];
       const float top = fmaxf(R, ml.x);
-      // (a part that saw nothing has R = -inf and zeros)
-      const float old = R == -INFINITY ? 0.f : ex2(R - top);
-      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - top);
+      // (a part that saw nothing has R = -inf and zeros, or NaN)
+      const float old = R == -INFINITY ? 1.f : ex2(R - top);
+      const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - top);
       R = top;
       l = fmaf(w, ml.y, l * old);
-      a.x = fmaf(w, x.x, a.x * old);
-      a.y = fmaf(w, x.y, a.y * old);
-      a.z = fmaf(w, x.z, a.z * old);
-      a.w = fmaf(w, x.w, a.w * old);
+      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[e]));
+        a[2 * e] = fmaf(w * ml.z, f.x, a[2 * e] * old);
+        a[2 * e + 1] = fmaf(w * ml.z, f.y, a[2 * e + 1] * old);
+      }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv),
-                                 __floats2bfloat162_rn(a.z * inv, a.w * inv)};
-    *reinterpret_cast<uint2*>(p.out + row * kLatent + 256 * th + 4 * piece) =
-        *reinterpret_cast<const uint2*>(o);
-    if (piece == 0 && th == 0 && p.lse)
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(a[2 * e] * inv, a[2 * e + 1] * inv);
+      o[e] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p.out + row * kLatent + d) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (d == 0 && p.lse)
       p.lse[row] = l != 0.f ? (R + log2f(l)) * 0.69314718055994530942f : -INFINITY;
   }
 }
@@ -1152,7 +1159,7 @@ cudaError_t launch(const AttnFp4Plan& pl, const KParams& p, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (pl.ws_bytes > 0) {
-    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, pl.units < 32 ? 32 : 8),
+    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, pl.units < 32 ? 16 : 4),
                   dim3(kJoinThreads), 0, stream,
                   true, 1, p);
     if (e != cudaSuccess) return e;
@@ -1183,7 +1190,7 @@ AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t
   pl.min_tiles = 1;
   if (tiles > 1)  // units of one tile are never split
     pl.ws_bytes = up256(pl.grid * sizeof(int2)) +
-                  static_cast<size_t>(2) * pl.grid * (kM * sizeof(float2) + kPartFloats * 4);
+                  static_cast<size_t>(2) * pl.grid * (kM * sizeof(float4) + kPartHalfs * 2);
   return pl;
 }
 
@@ -1211,9 +1218,9 @@ cudaError_t launch_attn_fp4(const AttnFp4Plan& pl, const AttnFp4Args& a, cudaStr
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     p.comb = reinterpret_cast<int2*>(ws);
     ws += up256(pl.grid * sizeof(int2));
-    p.part_ml = reinterpret_cast<float2*>(ws);
-    ws += static_cast<size_t>(2) * pl.grid * kM * sizeof(float2);
-    p.part_o = reinterpret_cast<float4*>(ws);
+    p.part_ml = reinterpret_cast<float4*>(ws);
+    ws += static_cast<size_t>(2) * pl.grid * kM * sizeof(float4);
+    p.part_o = reinterpret_cast<__half*>(ws);
   }
   return a.idx ? launch<true>(pl, p, stream) : launch<false>(pl, p, stream);
 }

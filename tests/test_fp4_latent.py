@@ -322,13 +322,16 @@ def _check(got, got_lse, q, rows, scale, splits_tokens, what):
     are off by at most 2^-25 in units where the largest w_t 2^E_t is 2^7 or more (E_t a
     row's exponent, or that of a row among its 8 neighbours, up to 4 larger): S of them,
     times values of at most 6 * 2^E_t <= 2^5 max |c_t|, are S * 2^-27 * max_t w_t max |c_t|
-    (2^E >= 2^-50 stands in for a row of zeros)."""
+    (2^E >= 2^-50 stands in for a row of zeros).  Where several CTAs share a row, each
+    one's part is rounded to fp16 once more, normalised by the sum of its w_t 2^E_t: 2^-11
+    of a value no larger than the mass, or 2^-25 of that sum (its subnormals), in all
+    2^-25 * S * 2^3 * max_t w_t max |c_t| by the same 2^E_t."""
     o, l, mass, reach, top = _softmax64(q, rows, scale)
     dz = 2.0 ** -14 * reach
     n_adds = splits_tokens / 16 + 64
-    rel = 2 * dz[:, None] + 2.0 ** -11 + 2.0 ** -19 + n_adds * 2.0 ** -23
+    rel = 2 * dz[:, None] + 2 * 2.0 ** -11 + 2.0 ** -19 + n_adds * 2.0 ** -23
     tol = 2.0 ** -8 * (np.abs(o) + rel * mass) + rel * mass + 1e-38 \
-        + rows.shape[0] * 2.0 ** -27 * top
+        + rows.shape[0] * (2.0 ** -27 + 2.0 ** -22) * top
     bad = ~(np.abs(got - o) <= tol)
     assert not bad.any(), (what, float(np.abs(got - o).max()), int(bad.sum()))
     if got_lse is not None:
@@ -706,11 +709,13 @@ def test_offsets_beyond_32_bits():
     tot = w.sum(-1) + (n - 40) * np.exp(-m)
     ref = (w @ vals) / tot[:, None]
     dz = 2.0 ** -14 * (np.abs(q) @ np.abs(vals).T).max(-1)
-    rel = 2 * dz[:, None] + 2.0 ** -11 + 2.0 ** -19 + (n / 148 / 16 + 64) * 2.0 ** -23
+    rel = 2 * dz[:, None] + 2 * 2.0 ** -11 + 2.0 ** -19 + (n / 148 / 16 + 64) * 2.0 ** -23
     mass = (w @ np.abs(vals)) / tot[:, None]
     # (only the 40 rows have values: the zero rows' weights multiply zeros)
     top = (w * np.abs(vals).max(-1)).max(-1, keepdims=True) / tot[:, None]
     tol = 2.0 ** -8 * (np.abs(ref) + rel * mass) + rel * mass + 40 * 2.0 ** -27 * top
+    # fp16 subnormals of a part: 2^-25 of its weights' sum in units of 2^E (E = 1 at most here)
+    tol = tol + 2.0 ** -25 * 2.0
     assert (np.abs(got[0] - ref) <= tol).all()
     # fp32 sums of up to 61,000 tokens a CTA in steps of a 64-token tile
     assert (np.abs(lse[0] - (m + np.log(tot))) <= dz + 2.0 ** -19 + 2.0 ** -12).all()
