@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
       const bool whole = (tm.bits & (kHead | kTail)) == (kHead | kTail);
       // A whole unit: out = O / l in bf16.  A part: O / (sum of its weights), at
-      // most 24 in magnitude, in fp16 (11 bits: a fifth of the output's own
+      // most 6 in magnitude, in fp16 (11 bits: a fifth of the output's own
       // rounding when joined; fp32 parts took twice the traffic).
       const float norm = whole ? l_run : w_run, inv = norm != 0.f ? 1.f / norm : 0.f;
       const int part_slot = 2 * blockIdx.x + ((tm.bits & kHead) ? 1 : 0);

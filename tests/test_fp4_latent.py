@@ -252,6 +252,48 @@ def test_append_padded_batch_and_bounds():
         assert np.array_equal(scales.cpu().numpy(), rs)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("ragged", [False, True])
+def test_append_and_read_many_rows(ragged):
+    """Enough rows for the kernels' form of several rows a warp, a ragged number of them."""
+    spx = need_gpu()
+    rng = np.random.default_rng(9)
+    B, n_new, cap = 7, 6001, 6011
+    base = _wild_rows(rng, 997)
+    pick = rng.integers(0, 997, (B, n_new))
+    rc, rs = oracle.latent_fp4(base)
+    vals = _bf16_bits(np.nan_to_num(oracle.dequant_fp4(rc, rs)))
+    nan = np.isnan(oracle.dequant_fp4(rc, rs))
+    lens = np.array([0, 10, 3, 5, 0, 7, 1], np.int64)
+    n_add = np.array([6001, 0, 1, 6000, 4002, 4003, 5999], np.int32)
+    k = n_add if ragged else np.full(B, n_new, np.int32)
+    codes = torch.full((B, cap, 256), 1, dtype=torch.uint8, device="cuda")
+    scales = torch.full((B, cap, 16), 2, dtype=torch.uint8, device="cuda")
+    spx.spx_latent_append_fp4(B, to_dev_bf16(base[pick]), n_new,
+                              torch.from_numpy(n_add).cuda() if ragged else None, codes, scales,
+                              cap, torch.from_numpy(lens).cuda(), cap)
+    gc, gs = codes.cpu().numpy(), scales.cpu().numpy()
+    for b in range(B):
+        at = slice(lens[b], lens[b] + k[b])
+        assert np.array_equal(gc[b, at], rc[pick[b, :k[b]]])
+        assert np.array_equal(gs[b, at], rs[pick[b, :k[b]]])
+        assert (gc[b, :lens[b]] == 1).all() and (gc[b, lens[b] + k[b]:] == 1).all()
+    n_vis = torch.from_numpy(lens + k).cuda()
+    pos = np.sort(rng.integers(0, cap, (B, n_new)), -1)
+    for p in (None, torch.from_numpy(pos).cuda()):
+        out = torch.full((B, n_new, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        spx.spx_latent_read_fp4(B, codes, scales, cap, p, n_new, n_vis, out)
+        got = bits_of(out)
+        for b in range(B):
+            want = pos[b] if p is not None else np.arange(n_new)
+            row = want - lens[b]
+            mine = (row >= 0) & (row < k[b])
+            src = pick[b, row[mine]]
+            assert np.array_equal(got[b][mine][~nan[src]], vals[src][~nan[src]])
+            assert np.isnan(oracle.bf16_to_f64(got[b][mine][nan[src]])).all()
+            assert (got[b][want >= lens[b] + k[b]] == 0).all()
+
+
 def _cache(rng, seqs, cap, lo=-3, hi=3):
     """A quantised cache of random rows (finite), as device arrays and values."""
     x = rng.standard_normal((seqs * cap, 512)) * np.exp2(rng.integers(lo, hi + 1, (seqs * cap, 1)))
