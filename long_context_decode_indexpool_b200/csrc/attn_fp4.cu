@@ -90,7 +90,6 @@ struct KParams {
   int heads, per_seq;
   int units, groups;       // groups of 64 heads per row (dense: or rgs > 1)
   int rows_per_unit, rgs;  // rows of a unit; units per (sequence, head group)
-  int min_tiles;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -99,16 +98,14 @@ struct KParams {
   __half* part_o;  // [2 grid][64][512] O / sum of the weights
 };
 
-// A tile as the list warp describes it to the other roles.
+// A slot's item as the list warps describe it to the other roles.
 struct __align__(16) TileMeta {
   int unit;
-  int tile;           // index in the unit
-  int bits;           // tokens in its part of the list (0..64), and flags
+  int bits;           // tokens of the tile's part of the list (0..64), and flags
   uint32_t valid[2];  // a bit per token that has a row in the cache
 };
-// first, last tile of its segment; the segment has the unit's first, last tile;
-// not a tile but its segment's queries
-enum : int { kFirst = 256, kLast = 512, kHead = 1024, kTail = 2048, kQueries = 4096 };
+// first, last tile of its segment; not a tile but its segment's queries
+enum : int { kFirst = 256, kLast = 512, kQueries = 1024 };
 
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -348,7 +345,7 @@ __device__ __forceinline__ Part plan_part(const KParams& p, int* scratch /* [kTh
   const int total = __reduce_add_sync(0xffffffffu, lane < kWarps ? scratch[lane] : 0);
   __syncthreads();
   const int g = static_cast<int>(gridDim.x);
-  part.quota = max((total - 1) / g + 1, p.min_tiles);
+  part.quota = (total - 1) / g + 1;
   const int64_t begin = static_cast<int64_t>(part.quota) * blockIdx.x;
   part.begin = static_cast<int>(begin < total ? begin : total);
   part.end = min(part.begin + min(part.quota, total - part.begin), total);
@@ -538,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     int seg = 0;  // segments begun
 #pragma unroll 1
     for (int t = 0; t < ntiles;) {
-      ok &= warp_wait(&bar_raw[slot.i], slot.parity, abort);
+      ok = __all_sync(0xffffffffu, warp_wait(&bar_raw[slot.i], slot.parity, abort));
+      if (!ok) break;
       const uint32_t base = slot_u + slot.i * kSlotBytes;
       const int bits = meta_s[slot.i].bits;
       if (bits & kQueries) {  // (the workers take them to TMEM)
@@ -546,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         ++seg;
       } else {
         ++t;
-        const bool valid = ok && ((meta_s[slot.i].valid[w >> 2] >> (8 * (w & 3) + r8)) & 1u);
+        const bool valid = ((meta_s[slot.i].valid[w >> 2] >> (8 * (w & 3) + r8)) & 1u) != 0;
         uint32_t c[4][4], sw[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // groups 4 (k ^ odd) + g4
@@ -706,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         comb = make_int2(u, (part.begin + t_end - 1) / part.quota - static_cast<int>(blockIdx.x) + 1);
     };
     int pos = 0, nt = 0;  // of this lane's block: first token, tokens (0..4)
+    int tok_t = 0;        // the tile's first list entry
     TileMeta m;
     auto request = [&](int t) {  // the blocks of tile t
       if (t >= t_end) {
@@ -715,12 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         t_end = t_org + tiles_of(un.S);
         enter_unit();
       }
+      tok_t = (t - t_org) * kTT;
       m.unit = u;
-      m.tile = t - t_org;
-      m.bits = max(0, min(un.S - m.tile * kTT, kTT)) | (t == max(t_org, 0) ? kFirst : 0) |
-               (t == min(t_end, ntiles) - 1 ? kLast : 0) | (t_org >= 0 ? kHead : 0) |
-               (t_end <= ntiles ? kTail : 0);
-      const int j = m.tile * kTT + (lane & 15) * kPool;
+      m.bits = max(0, min(un.S - tok_t, kTT)) | (t == max(t_org, 0) ? kFirst : 0) |
+               (t == min(t_end, ntiles) - 1 ? kLast : 0);
+      const int j = tok_t + (lane & 15) * kPool;
       pos = j;
       nt = max(0, min(un.S - j, kPool));
       if (kSparse && nt > 0) {
@@ -791,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       if (t + 1 < ntiles) {
         request(t + 1);
         if (!kSparse && lane == 0 && lw == 1 && (m.bits & 0xFF) > 0) {
-          const int64_t at = tok0 + m.tile * kTT;
+          const int64_t at = tok0 + tok_t;
           l2_prefetch(p.codes + at * kFp4CodeBytes, (m.bits & 0xFF) * kFp4CodeBytes);
           l2_prefetch(p.scales + at * kFp4Groups, (m.bits & 0xFF) * kFp4Groups);
         }
@@ -805,6 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     const int m = qd * 16 + (lane & 15);  // this thread's (row, head) pair of the unit
     const uint32_t tm_q = tmem + (static_cast<uint32_t>(qd * 32) << 16);  // this lane quarter
     const int hpr = min(p.heads, kM);
+    // The workers wait for one another at named barriers, which have no limit,
+    // so what they pass must not depend on a wait that may have given up: the
+    // segments' ends come from the units' lengths, not from the slots.
+    int u = part.u0, t_org = part.off0 - part.begin, seg_end = 0;  // seg_end: tiles of the segments begun
+    Unit un = load_unit<kSparse>(p, u);
     int seg = 0, row_lim = 0;
     int64_t out_row = -1;  // row of out of this thread, or -1
     float hs = 0.f, m_run = -INFINITY, l_run = 0.f, w_run = 0.f;  // w_run: sum of the weights
@@ -812,14 +815,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     for (int t = 0; t < ntiles;) {
       const int buf = t & 1;
       ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
-      const TileMeta tm = meta_s[slot.i];
-      if (ok && (tm.bits & kQueries)) {
+      if (t == seg_end) {
         // ---- the segment's queries: from their slot to TMEM ------------------
         hs = hs_s[seg & 3][m];
         ++seg;
         m_run = -INFINITY;
         l_run = w_run = 0.f;
-        const UnitRows ur = unit_rows<kSparse>(p, tm.unit);
+        if (t > 0) {
+          ++u;
+          t_org = t;
+          un = load_unit<kSparse>(p, u);
+        }
+        seg_end = min(t_org + tiles_of(un.S), ntiles);
+        const UnitRows ur = unit_rows<kSparse>(p, u);
         const int rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
         const bool mine = rr < ur.nrows && h < p.heads;
         out_row = mine ? static_cast<int64_t>(ur.row0 + rr) * p.heads + h : -1;
@@ -849,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         continue;
       }
       // (2^E, E) of this thread's two groups of 8 tokens
+      const uint32_t valid = meta_s[slot.i].valid[th];
       uint32_t oc[4];
       lds128(smem_u32(&oct_s[slot.i][4 * th + 2 * half]), oc);
       const bool own = __any_sync(0xffffffffu, oc[1] == 0x7F800000u || oc[3] == 0x7F800000u);
@@ -903,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         }
       }
       {
-        const int lim = row_lim - tm.tile * kTT - 32 * th - 16 * half;
-        uint32_t sees = (tm.valid[th] >> (16 * half)) & 0xFFFFu;
+        const int lim = row_lim - (t - t_org) * kTT - 32 * th - 16 * half;
+        uint32_t sees = (valid >> (16 * half)) & 0xFFFFu;
         if (lim < 16) sees &= (1u << max(lim, 0)) - 1u;
         if (__any_sync(0xffffffffu, sees != 0xFFFFu)) {
 #pragma unroll
@@ -973,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           // (queries, logits) with what they hold, so the products in flight
           // are waited for: PV(t-1), and QK(t+1) if the segment goes on.
           ok &= warp_wait(&bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
-          if (!(tm.bits & kLast))
+          if (t + 1 < seg_end)
             ok &= warp_wait(&bar_qk[(t + 1) & 1], ((t + 1) >> 1) & 1, abort);
           tc_fence_after();
 #pragma unroll 1
@@ -1004,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       if (lane == 0) mbar_arrive(&bar_p[buf]);
       const uint32_t pv_parity = (t >> 1) & 1;
       ++t;
-      if (!(tm.bits & kLast)) continue;
+      if (t < seg_end) continue;
 
       // ---- the segment's output (in lanes 16-31; a warp has 256 dims) --------
       w_run += __shfl_xor_sync(0xffffffffu, w_run, 16);
@@ -1015,12 +1024,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       ok &= warp_wait(&bar_pv[buf], pv_parity, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
-      const bool whole = (tm.bits & (kHead | kTail)) == (kHead | kTail);
+      const bool head = t_org >= 0, whole = head && t_org + tiles_of(un.S) <= ntiles;
       // A whole unit: out = O / l in bf16.  A part: O / (sum of its weights), at
       // most 6 in magnitude, in fp16 (11 bits: a fifth of the output's own
       // rounding when joined; fp32 parts took twice the traffic).
       const float norm = whole ? l_run : w_run, inv = norm != 0.f ? 1.f / norm : 0.f;
-      const int part_slot = 2 * blockIdx.x + ((tm.bits & kHead) ? 1 : 0);
+      const int part_slot = 2 * blockIdx.x + (head ? 1 : 0);
       const int64_t dst_row = whole ? out_row : static_cast<int64_t>(part_slot) * kM + m;
       uint16_t* const dst =
           whole ? reinterpret_cast<uint16_t*>(p.out) : reinterpret_cast<uint16_t*>(p.part_o);
@@ -1187,7 +1196,6 @@ AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t
   const int sms = num_sms < kMaxGrid ? num_sms : kMaxGrid;
   if (pl.units * tiles > 0x7fffffff) return AttnFp4Plan{};  // tiles are counted in 32 bits
   pl.grid = static_cast<int>(pl.units * tiles < sms ? pl.units * tiles : sms);
-  pl.min_tiles = 1;
   if (tiles > 1)  // units of one tile are never split
     pl.ws_bytes = up256(pl.grid * sizeof(int2)) +
                   static_cast<size_t>(2) * pl.grid * (kM * sizeof(float4) + kPartHalfs * 2);
@@ -1210,7 +1218,6 @@ cudaError_t launch_attn_fp4(const AttnFp4Plan& pl, const AttnFp4Args& a, cudaStr
   p.groups = pl.groups;
   p.rows_per_unit = pl.rows_per_unit;
   p.rgs = pl.rgs;
-  p.min_tiles = pl.min_tiles;
   p.scale_log2 = a.sm_scale * 1.44269504088896340736f;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;

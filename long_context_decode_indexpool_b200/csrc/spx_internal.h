@@ -202,8 +202,7 @@ cudaError_t launch_latent_read_fp4(int B, const uint8_t* codes, const uint8_t* s
 struct AttnFp4Plan {
   int units, groups;       // units of 64 (row, head) pairs; groups of 64 heads
   int rows_per_unit, rgs;  // rows of a unit; units per sequence and head group
-  int grid, min_tiles;     // CTAs (0: more tiles than the kernel counts); tiles of 64 tokens a
-                           // CTA takes, at least
+  int grid;                // CTAs (0: more tiles of 64 tokens than the kernel counts)
   size_t ws_bytes;
 };
 struct AttnFp4Args {

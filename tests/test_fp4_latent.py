@@ -524,6 +524,25 @@ def test_latent_attention_many_short_sequences():
 
 
 @pytest.mark.gpu
+def test_more_units_than_threads():
+    """Many rows of two head groups and of unequal lengths, some of them empty."""
+    spx = need_gpu()
+    rng = np.random.default_rng(27)
+    seqs, per, cap, heads = 300, 3, 200, 80
+    n_vis = rng.integers(0, cap + 1, seqs * per)
+    n_vis[rng.integers(0, seqs * per, 40)] = 0
+    codes, scales, vals = _cache(rng, seqs, cap)
+    d = spx.dims(heads, 0.9)
+    qb = synth.f32_to_bf16_bits_np((rng.standard_normal((seqs * per, heads, 512)) / 25)
+                                   .astype(np.float32))
+    got, lse = _run_latent(spx, d, per, to_dev_bf16(qb), codes, scales,
+                           torch.from_numpy(n_vis).cuda(), cap)
+    q = oracle.bf16_to_f64(qb)
+    for r in range(seqs * per):
+        _check(got[r], lse[r], q[r], vals[r // per][:n_vis[r]], 0.9, cap, f"row {r}")
+
+
+@pytest.mark.gpu
 def test_latent_attention_lengths_out_of_range():
     """Lengths are clamped to [0, min(max_len, cap_tok)]."""
     spx = need_gpu()
