@@ -6,7 +6,8 @@
 // (spx_latent_attn_fp4).
 //
 // Operands.  A cached row is c_t = 2^E_t c'_t, E_t its largest group exponent
-// and c'_t exact in fp16; a query head is q_h = 2^-s_h q'_h with max |q'_h| in
+// (or that of a row among its 8 neighbours, where all of them are within 4) and
+// c'_t exact in fp16; a query head is q_h = 2^-s_h q'_h with max |q'_h| in
 // [2^14, 2^15), exact in fp16 down to 2^-32 of that.  So
 //   z_t = log2(e) sm_scale 2^-s_h 2^E_t (q'_h . c'_t) + E_t   (base 2),
 //   P_t = 2^(z_t - R),  O = sum_t P_t c'_t,  l = sum_t P_t 2^-E_t,
@@ -23,22 +24,33 @@
 // in tiles of 64 tokens, form one sequence of tiles that is cut into equal
 // parts, one per CTA (one CTA per SM), whatever the lengths.  A CTA walks its
 // part as segments of units; a segment that is not its whole unit leaves its
-// O and (R, l) in fp32 in the workspace, and k_attn_fp4_combine joins them.
+// part in the workspace, and k_attn_fp4_combine joins the parts.
 //
-// One CTA: 8 worker warps (softmax, output), one MMA warp, 7 converter warps.
-// TMEM (an M = 64 accumulator puts row 16w+i in lane 32w+i, or 32w+16+i with
-// the lane offset 16):
-//   O dims   0-255: lanes 32w+i,    columns 0-255
-//   O dims 256-511: lanes 32w+16+i, columns 0-255
-//   S (64 tokens):  lanes 32w+16+i, columns 256+64b .. (b = S buffer 0/1)
-// Converter warps take groups of 8 tokens in turn (codes and scales are
-// loaded one group ahead, block ids two), multiply the codes up to fp16 in
-// registers and store them in the 128-byte-swizzle layout, double-buffered: a
-// buffer is refilled as soon as the PV of its previous tile is done.  The MMA
-// warp issues S = Q C^T (M = 64, N = 64, K = 16, 32 times) and O += P C (M =
-// 64, N = 256, K = 16, 8 times, C read MN-major from the same tile), whichever
-// is ready first.  A worker warp shares a TMEM lane quarter with another; each
-// takes 32 of a tile's tokens, the two threads of lanes i and 16+i a head.
+// One CTA, 20 warps, which pass items (a segment's queries, its tiles) through
+// three shared-memory slots of 64 KiB:
+//   list warps (2): the blocks of a tile and their positions; they copy its
+//     codes and scales (17 KiB, cp.async) into a slot as soon as it is free;
+//   converters (8): a warp expands its 8 tokens where they lie, from 4 bits to
+//     fp16 in the 128-byte-swizzle layout; they also bring the queries, which
+//     the workers take on to TMEM;
+//   QK warp: S = Q C^T, 32 tcgen05.mma (M = 64, N = 64, K = 16), A in TMEM;
+//   PV warp: O += P C, 8 tcgen05.mma (M = 64, N = 256, K = 16, C read MN-major
+//     from the same slot), which gives the slot back;
+//   workers (8): softmax and output.  A warp has 16 pairs and 32 of a tile's
+//     tokens, the two threads of lanes i and 16 + i a pair.
+// An M = 64 product uses 16 lanes of each TMEM quarter, so both halves of the
+// lanes are used: lanes 0-15 the queries (columns 0-255) and two buffers of S
+// (256-383), lanes 16-31 O (0-511).
+//
+// What bounds it.  An M = 64 product runs at half the tensor rate (2,048 cycles
+// a tile: 0.36 ms for four sequences of 0.5-1M tokens, where it takes 0.56); a
+// tile's operand reads (1,130 wavefronts of 128 bytes: the queries in TMEM save
+// 512), its expansion and copies (about 1,300) share one shared-memory port;
+// and a slot's round (copy, expand, QK, softmax, PV: about 10,000 cycles with
+// three in flight) sets the pace at 3,400 cycles a tile.  Tried and slower: two
+// slots and the queries in shared memory (4,200); the converters loading their
+// own rows into registers (3,800); bulk copies of 1 KiB blocks (the copy
+// engine takes 75 cycles each: 5,600); 16 warps with one list for all (5,000).
 #include <atomic>
 
 #include "latent_fp4.cuh"
