@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     tmem_relinquish();
   }
   pdl_trigger();
+  pdl_wait();  // (the set-up above ran beside the end of the stream's last kernel)
   const Part part = plan_part<kSparse>(p, scratch);
   const int ntiles = part.end - part.begin;
   tc_fence_before();
@@ -1110,6 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 constexpr int kJoinThreads = 256;
 template <bool kSparse>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_fp4_combine(const KParams p) {
+  pdl_trigger();
   pdl_wait();
   const int c = blockIdx.x, tid = threadIdx.x;
   const int2 cb = p.comb[c];
@@ -1176,7 +1178,7 @@ template <bool kSparse>
 cudaError_t launch(const AttnFp4Plan& pl, const KParams& p, cudaStream_t stream) {
   if (!set_attrs<kSparse>()) return cudaGetLastError();
   cudaError_t e = launch_ex(k_attn_fp4<kSparse>, dim3(pl.grid), dim3(kThreads), kSmemBytes, stream,
-                            false, 1, p);
+                            true, 1, p);
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (pl.ws_bytes > 0) {
