@@ -47,7 +47,10 @@
 // tile's operand reads (1,130 wavefronts of 128 bytes: the queries in TMEM save
 // 512), its expansion and copies (about 1,300) share one shared-memory port;
 // and a slot's round (copy, expand, QK, softmax, PV: about 10,000 cycles with
-// three in flight) sets the pace at 3,400 cycles a tile.  Tried and slower: two
+// three in flight) sets the pace at 3,400 cycles a tile.  Where units are short,
+// their joints count: the next unit's queries go to TMEM before the last one's
+// output is read from it, so that its first products run meanwhile (1,024 units
+// of 33 tiles: 497 us with the output first, 476 so).  Tried and slower: two
 // slots and the queries in shared memory (4,200); the converters loading their
 // own rows into registers (3,800); bulk copies of 1 KiB blocks (the copy
 // engine takes 75 cycles each: 5,600); 16 warps with one list for all (5,000).
@@ -211,6 +214,10 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                "r"(d)
                : "memory");
 }
+__device__ __forceinline__ void workers_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 5, %0;" ::"n"(kWork) : "memory");
+}
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* v) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
@@ -278,6 +285,17 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
       "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
       "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
       "r"(v[30]), "r"(v[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 16 lanes x 32 columns.
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -819,56 +837,61 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     // The workers wait for one another at named barriers, which have no limit,
     // so what they pass must not depend on a wait that may have given up: the
     // segments' ends come from the units' lengths, not from the slots.
-    int u = part.u0, t_org = part.off0 - part.begin, seg_end = 0;  // seg_end: tiles of the segments begun
-    Unit un = load_unit<kSparse>(p, u);
-    int seg = 0, row_lim = 0;
+    int u = part.u0, t_org = part.off0 - part.begin;  // CTA tiles t_org .. are unit u's
+    int seg = 0, seg_end = 0, tiles = 0, row_lim = 0;
     int64_t out_row = -1;  // row of out of this thread, or -1
     float hs = 0.f, m_run = -INFINITY, l_run = 0.f, w_run = 0.f;  // w_run: sum of the weights
+    // A segment's queries, from their slot to TMEM: 16-lane stores, which leave O
+    // in the other lanes alone, so that the segment's first products start while
+    // the last one's output is still written.  (Thread 4 r + c of a 16 x 256-bit
+    // store has columns 2 c, 2 c + 1 of rows r and r + 8.)
+    auto take_queries = [&] {
+      ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+      const float next_hs = hs_s[seg & 3][m];
+      ++seg;
+#pragma unroll 1
+      for (int r = 4 * th; r < 4 * th + 4; ++r) {  // 64 dims: 32 columns
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = qd * 16 + (lane >> 2) + 8 * (i & 1), piece = (i & 6) + ((lane & 3) >> 1);
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(v[2 * i]), "=r"(v[2 * i + 1])
+                       : "r"(slot_u + slot.i * kSlotBytes + r * kRegion + row * 128 +
+                             ((piece ^ (row & 7)) << 4) + 8 * (lane & 1))
+                       : "memory");
+        }
+        tmem_st_16x256b_x4(tm_q + 32 * r, v);
+      }
+      tc_fence_before();
+      workers_sync();  // every worker's part is there
+      if (tid == 0) {
+        mbar_arrive(&bar_q);
+        mbar_arrive(&bar_free[slot.i]);
+      }
+      slot.next();
+      return next_hs;
+    };
+    auto enter_segment = [&] {  // unit u's part of this CTA
+      const Unit un = load_unit<kSparse>(p, u);
+      tiles = tiles_of(un.S);
+      seg_end = min(t_org + tiles, ntiles);
+      m_run = -INFINITY;
+      l_run = w_run = 0.f;
+      const UnitRows ur = unit_rows<kSparse>(p, u);
+      const int rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
+      const bool mine = rr < ur.nrows && h < p.heads;
+      out_row = mine ? static_cast<int64_t>(ur.row0 + rr) * p.heads + h : -1;
+      // rows of one unit may see different numbers of tokens
+      row_lim = !kSparse && p.rows_per_unit > 1 ? (mine ? clamp_len(p, ur.row0 + rr) : 0)
+                                                : 0x7fffffff;
+    };
+    enter_segment();
+    hs = take_queries();
 #pragma unroll 1
     for (int t = 0; t < ntiles;) {
       const int buf = t & 1;
       ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
-      if (t == seg_end) {
-        // ---- the segment's queries: from their slot to TMEM ------------------
-        hs = hs_s[seg & 3][m];
-        ++seg;
-        m_run = -INFINITY;
-        l_run = w_run = 0.f;
-        if (t > 0) {
-          ++u;
-          t_org = t;
-          un = load_unit<kSparse>(p, u);
-        }
-        seg_end = min(t_org + tiles_of(un.S), ntiles);
-        const UnitRows ur = unit_rows<kSparse>(p, u);
-        const int rr = pair_row(m, hpr), h = ur.hg * kM + m - rr * hpr;
-        const bool mine = rr < ur.nrows && h < p.heads;
-        out_row = mine ? static_cast<int64_t>(ur.row0 + rr) * p.heads + h : -1;
-        // rows of one unit may see different numbers of tokens
-        row_lim = !kSparse && p.rows_per_unit > 1 ? (mine ? clamp_len(p, ur.row0 + rr) : 0)
-                                                  : 0x7fffffff;
-        // (the copy runs over the other half of the lanes, which hold O: both
-        // warps of the quarter have read the last segment's)
-        tc_fence_before();
-        pair_sync(qd);
-        tc_fence_after();
-#pragma unroll 1
-        for (int r = 4 * th; r < 4 * th + 4; ++r) {  // 64 dims: 32 columns
-          const uint32_t src = slot_u + slot.i * kSlotBytes + r * kRegion + m * 128;
-          uint32_t v[32];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) lds128(src + ((c ^ (m & 7)) << 4), v + 4 * c);
-          tmem_st_x32(tm_q + 32 * r, v);
-        }
-        tc_fence_before();
-        asm volatile("bar.sync 5, 256;" ::: "memory");  // every worker's part is there
-        if (tid == 0) {
-          mbar_arrive(&bar_q);
-          mbar_arrive(&bar_free[slot.i]);
-        }
-        slot.next();
-        continue;
-      }
       // (2^E, E) of this thread's two groups of 8 tokens
       const uint32_t valid = meta_s[slot.i].valid[th];
       uint32_t oc[4];
@@ -1034,10 +1057,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       pair_sync(qd);
       l_run += red_l[th ^ 1][m].x;
       w_run += red_l[th ^ 1][m].y;
+      // The next segment's queries first.  (Both warps of the quarter are behind
+      // their last scaling of O, which rewrites the queries' lanes too.)
+      if (t < ntiles) hs = take_queries();
       ok &= warp_wait(&bar_pv[buf], pv_parity, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
-      const bool head = t_org >= 0, whole = head && t_org + tiles_of(un.S) <= ntiles;
+      const bool head = t_org >= 0, whole = head && t_org + tiles <= ntiles;
       // A whole unit: out = O / l in bf16.  A part: O / (sum of its weights), at
       // most 6 in magnitude, in fp16 (11 bits: a fifth of the output's own
       // rounding when joined; fp32 parts took twice the traffic).
@@ -1054,10 +1080,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         tmem_ld_x32_async(tm_q + 256 * th + c0 + 32, raw + 32);
         tmem_ld_wait_regs<64>(raw);
         const float* v = reinterpret_cast<const float*>(raw);
-        // 16 rows of 64 dims through 2 KiB of the P buffers (idle until every
-        // worker has passed the next segment's queries), so that eight lanes
-        // store a row's 128 bytes: stores straight from the lanes of TMEM's
-        // rows took 5,500 cycles a segment.
+        // 16 rows of 64 dims through 2 KiB of the P buffers (the segment's last PV
+        // is done, the next tile's P waits for every worker), so that eight
+        // lanes store a row's 128 bytes.
         const uint32_t stage = p_u + warp * 2048;
         if (half == 1) {
 #pragma unroll
@@ -1092,7 +1117,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
                                         : -INFINITY;
       }
-      tc_fence_before();  // O is read before the next segment's queries and first PV
+      tc_fence_before();  // O is read before the next segment's first PV
+      if (t < ntiles) {
+        workers_sync();  // (the staging areas are others' P)
+        ++u;
+        t_org = t;
+        enter_segment();
+      }
     }
   }
   if (!ok && lane == 0) atomicExch(&g_device_error, kErrWaitTimeout);
