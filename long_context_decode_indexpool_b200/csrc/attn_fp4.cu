@@ -346,7 +346,7 @@ __device__ __forceinline__ Unit load_unit(const KParams& p, int u) {
   return x;
 }
 // A unit without tokens still has one tile: its rows' outputs are written.
-__device__ __forceinline__ int tiles_of(int S) { return max(1, (S + kTT - 1) / kTT); }
+__device__ __forceinline__ int tiles_of(int S) { return (max(S, 1) - 1) / kTT + 1; }
 
 // The part of the tile sequence a CTA owns, as every thread learns it.
 struct Part {
@@ -594,12 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         // than 4 below it (they are then still exact: 2^-1 2^-15 2^-4 is above
         // fp16's last bit, and P loses at most 4 of its 31 bits below the
         // largest term); otherwise each row has its own.
+        // A NaN group is NaN in its row's own E, not in the products' operand: 0
+        // weights (of a unit's rows that do not see it) would spread it there.
+        const bool nan = valid && __vcmpeq4(mine, 0xFFFFFFFFu) != 0;
         const int top = __reduce_max_sync(0xffffffffu, valid ? eb : 1);
-        const bool wide = top - __reduce_min_sync(0xffffffffu, valid ? eb : top) > kNear;
+        const bool wide =
+            top - __reduce_min_sync(0xffffffffu, nan ? -kNear : (valid ? eb : top)) > kNear;
         const int ref = wide ? eb : top;
-        if (wide && g4 == 0) {
-          tf_s[slot.i][w * kOct + r8] = __int_as_float(ref << 23);
-          te_s[slot.i][w * kOct + r8] = static_cast<float>(ref - 127);
+        if (wide) {
+          const bool row_nan = ((__ballot_sync(0xffffffffu, nan) >> (4 * r8)) & 0xFu) != 0;
+          if (g4 == 0) {
+            tf_s[slot.i][w * kOct + r8] = __int_as_float(ref << 23);
+            te_s[slot.i][w * kOct + r8] =
+                row_nan ? __int_as_float(0x7FFFFFFF) : static_cast<float>(ref - 127);
+          }
         }
         if (lane == 0)
           oct_s[slot.i][w] = wide ? make_float2(0.f, INFINITY)
@@ -613,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int b = static_cast<int>(((odd ? sw[k ^ 1] : sw[k]) >> (8 * g4)) & 0xFFu);
-            // 2^(e - E) in fp16 (0 from 2^-25 down; NaN for a NaN group; 0 where
+            // 2^(e - E) in fp16 (0 from 2^-25 down, for a NaN group and where
             // there is no token)
-            __half sc = __float2half_rn(__int_as_float(max(127 + b - ref, 97) << 23));
-            if (b == kFp4NanByte) sc = __ushort_as_half(0x7E00);
-            const __half2 s2 = __half2half2(valid ? sc : __ushort_as_half(0));
+            const __half sc = __float2half_rn(__int_as_float(max(127 + b - ref, 97) << 23));
+            const __half2 s2 =
+                __half2half2(valid && b != kFp4NanByte ? sc : __ushort_as_half(0));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t h[4];

@@ -641,6 +641,29 @@ def test_attention_propagates_nan():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads", [16, 32, 64])
+@pytest.mark.parametrize("lens", [(100, 101, 102, 103), (63, 64, 65, 130), (1, 0, 3, 200)])
+def test_nan_seen_by_the_later_rows_of_a_sequence_only(heads, lens):
+    """Rows of a sequence that see different lengths: a NaN group (or a row of
+    them) behind a row's length does not reach its output."""
+    spx = need_gpu()
+    rng = np.random.default_rng(22)
+    n = max(lens)
+    codes, scales, vals = _cache(rng, 1, n)
+    scales[0, sorted(lens)[-2], 3] = 255  # the row of the most tokens sees both
+    scales[0, n - 1] = 255
+    qb = synth.f32_to_bf16_bits_np((rng.standard_normal((4, heads, 512)) / 25).astype(np.float32))
+    d = spx.dims(heads, 1.0)
+    got, lse = _run_latent(spx, d, 4, to_dev_bf16(qb), codes, scales,
+                           torch.tensor(lens, dtype=torch.int64, device="cuda"), n)
+    for r in range(4):
+        if lens[r] == n:
+            assert np.isnan(got[r]).all() and np.isnan(lse[r]).all()
+        else:
+            _check(got[r], lse[r], oracle.bf16_to_f64(qb)[r], vals[0][:lens[r]], 1.0, n, f"row {r}")
+
+
+@pytest.mark.gpu
 def test_lse_is_optional_and_calls_repeat_bit_for_bit():
     spx = need_gpu()
     rng = np.random.default_rng(22)
