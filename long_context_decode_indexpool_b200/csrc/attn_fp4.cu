@@ -582,10 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           lds128(base + ((raw_off + 128 * (k >> 1)) ^ (64 * (k & 1))), c[k]);
         lds128(base + w * 1024 + 2 * kRegion + r8 * 16, sw);
         // the row's largest exponent byte but 255 (a NaN group): bytes + 1 mod
-        // 256, a word of four per lane
+        // 256, a word of four per lane; the bytes' carries are the NaN groups
         const uint32_t mine = swap ? (g4 & 1 ? sw[3] : sw[2]) : (g4 & 1 ? sw[1] : sw[0]);
-        uint32_t mx = __vmaxu2(((mine & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu,
-                               (((mine >> 8) & 0x00FF00FFu) + 0x00010001u) & 0x00FF00FFu);
+        const uint32_t lo1 = (mine & 0x00FF00FFu) + 0x00010001u;
+        const uint32_t hi1 = ((mine >> 8) & 0x00FF00FFu) + 0x00010001u;
+        const bool nan = ((lo1 | hi1) & 0x01000100u) != 0;
+        uint32_t mx = __vmaxu2(lo1 & 0x00FF00FFu, hi1 & 0x00FF00FFu);
         mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // (the raw rows are read)
         // biased exponent of the row, kept where 2^E and 2^-E are normal
@@ -594,15 +596,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
         // than 4 below it (they are then still exact: 2^-1 2^-15 2^-4 is above
         // fp16's last bit, and P loses at most 4 of its 31 bits below the
         // largest term); otherwise each row has its own.
-        // A NaN group is NaN in its row's own E, not in the products' operand: 0
-        // weights (of a unit's rows that do not see it) would spread it there.
-        const bool nan = valid && __vcmpeq4(mine, 0xFFFFFFFFu) != 0;
         const int top = __reduce_max_sync(0xffffffffu, valid ? eb : 1);
-        const bool wide =
-            top - __reduce_min_sync(0xffffffffu, nan ? -kNear : (valid ? eb : top)) > kNear;
+        const int low = __reduce_min_sync(0xffffffffu, valid ? (nan ? -kNear : eb) : top);
+        const bool wide = top - low > kNear;
         const int ref = wide ? eb : top;
         if (wide) {
+          // A NaN group is NaN in its row's own E, and any number in the products'
+          // operand: a NaN there would reach the rows of the unit that do not see
+          // it (their weight is 0).
           const bool row_nan = ((__ballot_sync(0xffffffffu, nan) >> (4 * r8)) & 0xFu) != 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sw[k] &= ~__vcmpeq4(sw[k], 0x01010101u * kFp4NanByte);
           if (g4 == 0) {
             tf_s[slot.i][w * kOct + r8] = __int_as_float(ref << 23);
             te_s[slot.i][w * kOct + r8] =
@@ -621,11 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int b = static_cast<int>(((odd ? sw[k ^ 1] : sw[k]) >> (8 * g4)) & 0xFFu);
-            // 2^(e - E) in fp16 (0 from 2^-25 down, for a NaN group and where
-            // there is no token)
-            const __half sc = __float2half_rn(__int_as_float(max(127 + b - ref, 97) << 23));
-            const __half2 s2 =
-                __half2half2(valid && b != kFp4NanByte ? sc : __ushort_as_half(0));
+            // 2^(e - E) in fp16 (0 from 2^-25 down; where there is no token the
+            // codes are zeros)
+            const __half2 s2 = __half2half2(
+                __float2half_rn(__int_as_float(max(127 + b - ref, 97) << 23)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t h[4];
