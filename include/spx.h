@@ -382,10 +382,11 @@ SPX_API spx_status spx_sparse_mla_attn_fp8(const spx_dims* d, int32_t rows, cons
  * ws: spx_latent_attn_fp4_workspace_size bytes for the same rows,
  * rows_per_seq and max_len.
  *
- * A row that sees no token gives out = 0 and lse = -inf.  The queries are
- * expected to be finite.  The cache arrays may be pinned host memory mapped
- * into the device's address space.  A workspace belongs to one call at a
- * time; calls that may overlap on the GPU need one each.
+ * A row that sees no token gives out = 0 and lse = -inf; one that sees a NaN
+ * group gives NaN, the others do not.  The queries are expected to be finite.
+ * The cache arrays may be pinned host memory mapped into the device's address
+ * space.  A workspace belongs to one call at a time; calls that may overlap on
+ * the GPU need one each.
  * ------------------------------------------------------------------------- */
 SPX_API spx_status spx_latent_append_fp4(int32_t B, const void* latent, int64_t n_new,
                                          const int32_t* n_add, void* codes, void* scales,

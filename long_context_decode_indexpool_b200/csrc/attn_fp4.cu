@@ -43,7 +43,7 @@
 // (256-383), lanes 16-31 O (0-511).
 //
 // What bounds it.  An M = 64 product runs at half the tensor rate (2,048 cycles
-// a tile: 0.36 ms for four sequences of 0.5-1M tokens, where it takes 0.56); a
+// a tile: 0.36 ms for four sequences of 0.5-1M tokens, where it takes 0.57); a
 // tile's operand reads (1,130 wavefronts of 128 bytes: the queries in TMEM save
 // 512), its expansion and copies (about 1,300) share one shared-memory port;
 // and a slot's round (copy, expand, QK, softmax, PV: about 10,000 cycles with
