@@ -445,6 +445,28 @@ def test_sparse_attention(heads, lens, shared):
 
 
 @pytest.mark.gpu
+def test_sparse_attention_odd_selections():
+    """Ids in any order, the same block twice (its tokens count twice), counts
+    below zero and above the row's blocks."""
+    spx = need_gpu()
+    rng = np.random.default_rng(31)
+    heads, n = 48, 1203
+    codes, scales, vals = _cache(rng, 1, n)
+    idx = rng.integers(0, n // 4, (4, 512)).astype(np.int32)
+    idx[0, :3] = 7
+    cnt = np.array([200, 300, -5, 600], np.int32)
+    qb = synth.f32_to_bf16_bits_np((rng.standard_normal((4, heads, 512)) / 20).astype(np.float32))
+    got, lse = _run_sparse(spx, spx.dims(heads, 1.0), to_dev_bf16(qb), codes, scales, 0, n,
+                           torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                           torch.full((4,), n, dtype=torch.int64, device="cuda"), n)
+    q = oracle.bf16_to_f64(qb)
+    for r, k in enumerate([200, 300, 0, n // 4]):
+        blocks = (4 * idx[r, :k, None] + np.arange(4)).reshape(-1)
+        c = vals[0][np.concatenate([blocks, np.arange(n // 4 * 4, n)])]
+        _check(got[r], lse[r], q[r], c, 1.0, 2051, f"row {r}")
+
+
+@pytest.mark.gpu
 def test_sparse_attention_many_rows():
     """A causal chunk on a shared cache: more rows than the device has SMs."""
     spx = need_gpu()
