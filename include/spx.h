@@ -380,7 +380,12 @@ SPX_API spx_status spx_sparse_mla_attn_fp8(const spx_dims* d, int32_t rows, cons
  * rows_per_seq rows of a sequence (draft tokens, a short causal chunk) share
  * its cache [rows / rows_per_seq, cap_tok, ..].  Other arguments as above;
  * ws: spx_latent_attn_fp4_workspace_size bytes for the same rows,
- * rows_per_seq and max_len.
+ * rows_per_seq and max_len.  SPX_ERR_UNSUPPORTED where the lists of all units
+ * of 64 (row, head) pairs may hold more than 2^31 - 1 tiles of 64 tokens.
+ *
+ * Both attention calls clamp n_vis to [0, min(max_len, cap_tok)], so max_len may
+ * be any bound from 0 to INT64_MAX, here and in the workspace's size (which
+ * stays the same from 2^31 - 1 on).
  *
  * A row that sees no token gives out = 0 and lse = -inf; one that sees a NaN
  * group gives NaN, the others do not.  The queries are expected to be finite.

@@ -1245,13 +1245,13 @@ AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t
   if (pl.rows_per_unit > per_seq) pl.rows_per_unit = per_seq;
   pl.rgs = (per_seq + pl.rows_per_unit - 1) / pl.rows_per_unit;
   pl.units = rows / per_seq * pl.rgs * pl.groups;  // (at most 2 x 65535)
-  int64_t list = max_len;  // tokens in a list, at most
+  int64_t list = max_len < kFp4MaxTok ? max_len : kFp4MaxTok;  // tokens in a list, at most
   if (sparse && list > kTopK * kPool + kPool - 1) list = kTopK * kPool + kPool - 1;
   int64_t tiles = (list + kTT - 1) / kTT;
   if (tiles < 1) tiles = 1;
   const int sms = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-  if (pl.units * tiles > 0x7fffffff) return AttnFp4Plan{};  // tiles are counted in 32 bits
-  pl.grid = static_cast<int>(pl.units * tiles < sms ? pl.units * tiles : sms);
+  pl.tiles = pl.units * tiles;  // (below 2^43)
+  pl.grid = static_cast<int>(pl.tiles < sms ? pl.tiles : sms);
   if (tiles > 1)  // units of one tile are never split
     pl.ws_bytes = up256(pl.grid * sizeof(int2)) +
                   static_cast<size_t>(2) * pl.grid * (kM * sizeof(float4) + kPartHalfs * 2);

@@ -13,7 +13,7 @@ spx_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SPX_OK : SPX_E
 
 // Token positions fit 31 bits and sequences 16, so that byte offsets into a
 // cache stay far below 2^63.
-constexpr int64_t kMaxTok = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTok = kFp4MaxTok;
 constexpr int32_t kMaxSeqs = 65535;
 constexpr int64_t kMaxRows = int64_t(1) << 33;  // rows of one write or read: 8 TiB
 
@@ -28,8 +28,10 @@ spx_status attn_fp4(const spx_dims* d, int32_t rows, int32_t per_seq, const void
   if (!al(q, 16) || !al(codes, 16) || !al(scales, 16) || !al(out, 16) || !al(n_vis, 8) ||
       (lse && !al(lse, 4)) || (sparse && (!al(idx, 4) || !al(count, 4))))
     return SPX_ERR_INVALID_ARG;
-  const AttnFp4Plan p = plan_attn_fp4(rows, per_seq, d->heads, sparse, max_len, device_sm_count());
-  if (p.grid == 0) return SPX_ERR_UNSUPPORTED;
+  // the plan's bound on the lengths is the one that the kernel clamps them to
+  const int64_t len_cap = max_len < cap_tok ? max_len : cap_tok;
+  const AttnFp4Plan p = plan_attn_fp4(rows, per_seq, d->heads, sparse, len_cap, device_sm_count());
+  if (p.tiles > 0x7fffffff) return SPX_ERR_UNSUPPORTED;
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes || !al(ws, 16))) return SPX_ERR_WORKSPACE;
   AttnFp4Args a{};
   a.rows = rows;
@@ -39,7 +41,7 @@ spx_status attn_fp4(const spx_dims* d, int32_t rows, int32_t per_seq, const void
   a.codes = static_cast<const uint8_t*>(codes);
   a.scales = static_cast<const uint8_t*>(scales);
   a.seq_tok = seq_tok;
-  a.len_cap = max_len < cap_tok ? max_len : cap_tok;
+  a.len_cap = len_cap;
   a.idx = sparse ? idx : nullptr;
   a.count = sparse ? count : nullptr;
   a.n_vis = n_vis;
@@ -91,9 +93,7 @@ spx_status spx_attn_fp4_workspace_size(const spx_dims* d, int32_t rows, int64_t 
   if (st != SPX_OK) return st;
   if (!bytes) return SPX_ERR_INVALID_ARG;
   if (rows < 1 || rows > 65535 || max_len < 0) return SPX_ERR_SHAPE;
-  const AttnFp4Plan p = plan_attn_fp4(rows, 1, d->heads, true, max_len, device_sm_count());
-  if (p.grid == 0) return SPX_ERR_UNSUPPORTED;
-  *bytes = p.ws_bytes;
+  *bytes = plan_attn_fp4(rows, 1, d->heads, true, max_len, device_sm_count()).ws_bytes;
   return SPX_OK;
 }
 
@@ -121,10 +121,7 @@ spx_status spx_latent_attn_fp4_workspace_size(const spx_dims* d, int32_t rows,
   if (!bytes) return SPX_ERR_INVALID_ARG;
   if (rows < 1 || rows > 65535 || max_len < 0) return SPX_ERR_SHAPE;
   if (rows_per_seq < 1 || rows % rows_per_seq != 0) return SPX_ERR_SHAPE;
-  const AttnFp4Plan p =
-      plan_attn_fp4(rows, rows_per_seq, d->heads, false, max_len, device_sm_count());
-  if (p.grid == 0) return SPX_ERR_UNSUPPORTED;
-  *bytes = p.ws_bytes;
+  *bytes = plan_attn_fp4(rows, rows_per_seq, d->heads, false, max_len, device_sm_count()).ws_bytes;
   return SPX_OK;
 }
 

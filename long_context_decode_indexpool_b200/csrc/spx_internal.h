@@ -199,10 +199,13 @@ cudaError_t launch_latent_append_fp4(int B, const void* lat, int64_t n_new, cons
 cudaError_t launch_latent_read_fp4(int B, const uint8_t* codes, const uint8_t* scales,
                                    int64_t cap_tok, const int64_t* pos, int64_t m,
                                    const int64_t* n_vis, void* out, cudaStream_t stream);
+// Most tokens a sequence's 4-bit cache holds: token positions fit 31 bits.
+constexpr int64_t kFp4MaxTok = (int64_t(1) << 31) - 1;
 struct AttnFp4Plan {
   int units, groups;       // units of 64 (row, head) pairs; groups of 64 heads
   int rows_per_unit, rgs;  // rows of a unit; units per sequence and head group
-  int grid;                // CTAs (0: more tiles of 64 tokens than the kernel counts)
+  int grid;                // CTAs
+  int64_t tiles;           // of 64 tokens, in all; the kernel counts 2^31 - 1 at most
   size_t ws_bytes;
 };
 struct AttnFp4Args {
@@ -220,6 +223,8 @@ struct AttnFp4Args {
   float* lse;
   void* ws;
 };
+// max_len: no row sees more tokens (any value; a cache's kFp4MaxTok at most
+// count).  The workspace never shrinks as it grows.
 AttnFp4Plan plan_attn_fp4(int rows, int per_seq, int heads, bool sparse, int64_t max_len,
                           int num_sms);
 cudaError_t launch_attn_fp4(const AttnFp4Plan& p, const AttnFp4Args& a, cudaStream_t stream);

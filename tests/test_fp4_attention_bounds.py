@@ -1,0 +1,85 @@
+"""Attention over the 4-bit latent cache where its bounds are met: lengths
+without a bound, on the CPU (sizes and refusals) and on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from _gpu_helpers import need_gpu, to_dev_bf16
+
+FAKE = 1 << 20  # an aligned non-null address; never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from conftest import build_lib
+    build_lib()
+    import long_context_decode_indexpool_b200 as m
+    return m
+
+
+# ---------------------------------------------------------------------------
+# max_len without a bound
+# ---------------------------------------------------------------------------
+HUGE = (2 ** 31, 2 ** 40, 2 ** 57, 2 ** 62, 2 ** 63 - 128, 2 ** 63 - 64, 2 ** 63 - 63, 2 ** 63 - 1)
+
+
+@pytest.mark.parametrize("rows,per", [(1, 1), (4, 2), (63, 1), (64, 1), (65, 1), (128, 64),
+                                      (65535, 65535)])
+def test_workspace_of_any_length(lib, rows, per):
+    for heads in (16, 64, 128):
+        d = lib.dims(heads, 1.0)
+        sizes = [lib.spx_latent_attn_fp4_workspace_size(d, rows, per, n)
+                 for n in (0, 1, 64, 65, 5000, 2 ** 20, 2 ** 31 - 1)]
+        assert sizes == sorted(sizes) and 0 < sizes[-1] < 1 << 26
+        for n in HUGE:
+            assert lib.spx_latent_attn_fp4_workspace_size(d, rows, per, n) == sizes[-1], n
+        if per == 1:
+            most = lib.spx_attn_fp4_workspace_size(d, rows, 2 ** 31 - 1)
+            for n in HUGE:
+                assert lib.spx_attn_fp4_workspace_size(d, rows, n) == most, n
+
+
+@pytest.mark.parametrize("max_len", HUGE)
+def test_calls_of_any_length_check_the_workspace(lib, max_len):
+    """A call whose rows may be shared by several CTAs wants the workspace for
+    that, whatever bound it is given; nothing is launched without it."""
+    d = lib.dims(64, 1.0)
+    for rows in (1, 63, 64, 65, 100):
+        for cap in (8192, 2 ** 31 - 1):
+            with pytest.raises(lib.SpxError) as e:
+                lib.spx_latent_attn_fp4(d, rows, 1, FAKE, FAKE, FAKE, cap, FAKE, max_len, FAKE,
+                                        None, None, 0, stream=0)
+            # more than 2^31 - 1 tiles: 64 rows of 2^31 - 1 tokens and up
+            assert e.value.status == (3 if cap > 8192 and rows >= 64 else 4), (rows, cap)
+        with pytest.raises(lib.SpxError) as e:
+            lib.spx_sparse_mla_attn_fp4(d, rows, FAKE, FAKE, FAKE, 0, 8192, FAKE, FAKE, FAKE,
+                                        max_len, FAKE, None, None, 0, stream=0)
+        assert e.value.status == 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 65])
+def test_no_bound_is_the_cache_s_own(rows):
+    """max_len = INT64_MAX gives bit for bit what max_len = cap_tok gives."""
+    spx = need_gpu()
+    rng = np.random.default_rng(40 + rows)
+    cap, d = 700, spx.dims(64, 1.0)
+    codes, scales = oracle.latent_fp4(
+        synth.f32_to_bf16_bits_np(rng.standard_normal((cap, 512)).astype(np.float32)))
+    codes = torch.from_numpy(codes).cuda().expand(rows, -1, -1).contiguous()
+    scales = torch.from_numpy(scales).cuda().expand(rows, -1, -1).contiguous()
+    q = to_dev_bf16(synth.f32_to_bf16_bits_np(
+        (rng.standard_normal((rows, 64, 512)) / 22).astype(np.float32)))
+    n_vis = torch.from_numpy(rng.integers(0, 2 * cap, rows)).cuda()
+    got = []
+    for max_len in (cap, 2 ** 63 - 64, 2 ** 63 - 1):
+        ws = spx.workspace(spx.spx_latent_attn_fp4_workspace_size(d, rows, 1, max_len), "cuda")
+        out, lse = torch.empty_like(q), torch.empty(rows, 64, device="cuda")
+        spx.spx_latent_attn_fp4(d, rows, 1, q, codes, scales, cap, n_vis, max_len, out, lse, ws)
+        torch.cuda.synchronize()
+        assert spx.spx_device_error() == 0
+        got.append((out, lse))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
