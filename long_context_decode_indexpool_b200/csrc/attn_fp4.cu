@@ -87,6 +87,7 @@ constexpr int kColS = 256;
 constexpr int kNear = 4;        // exponents of 8 rows that share one reference, at most apart
 constexpr float kLazy = 8.f;   // the maximum is raised when exceeded by more
 constexpr float kLift = 7.f;   // P = 2^(z - max + 7)
+constexpr float kPartScale = 8192.f;  // 2^13: a part of O, at most 6 in magnitude, in fp16
 constexpr int kMaxGrid = 160;  // CTAs (one per SM, at most)
 constexpr int kPartHalfs = kM * kLatent;
 constexpr uint32_t kIdescF16 = (1u << 4) | (static_cast<uint32_t>(kM >> 4) << 24);  // f16 A, B; f32 D
@@ -109,8 +110,8 @@ struct KParams {
   __nv_bfloat16* out;
   float* lse;
   int2* comb;      // [grid] (unit, CTAs it spans) of the split unit that begins in a CTA
-  float4* part_ml; // [2 grid][64] (R, l, sum of the weights)
-  __half* part_o;  // [2 grid][64][512] O / sum of the weights
+  float4* part_ml; // [2 grid][64] (R, l, sum of the weights / kPartScale)
+  __half* part_o;  // [2 grid][64][512] kPartScale O / sum of the weights
 };
 
 // A slot's item as the list warps describe it to the other roles.
@@ -1076,9 +1077,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
       const bool head = t_org >= 0, whole = head && t_org + tiles <= ntiles;
       // A whole unit: out = O / l in bf16.  A part: O / (sum of its weights), at
-      // most 6 in magnitude, in fp16 (11 bits: a fifth of the output's own
-      // rounding when joined; fp32 parts took twice the traffic).
-      const float norm = whole ? l_run : w_run, inv = norm != 0.f ? 1.f / norm : 0.f;
+      // most 6 in magnitude, times 2^13 in fp16: 11 bits down to 2^-27 (an eighth
+      // of the output's own rounding; fp32 parts took twice the traffic).  A row's
+      // smallest groups lie 2^15 below its largest, and up to 2^19 below the
+      // exponent it is held with, and a mean over tokens is smaller again: without
+      // the factor they ended in fp16's subnormals (means of 2^-20 were off by up
+      // to 3.5 % in rows that CTAs share).
+      const float norm = whole ? l_run : w_run;
+      const float inv = norm != 0.f ? (whole ? 1.f : kPartScale) / norm : 0.f;
       const int part_slot = 2 * blockIdx.x + (head ? 1 : 0);
       const int64_t dst_row = whole ? out_row : static_cast<int64_t>(part_slot) * kM + m;
       uint16_t* const dst =
@@ -1123,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       }
       if (half == 0 && th == 0) {
         if (!whole)
-          p.part_ml[part_slot * kM + m] = make_float4(ref_out, l_run, w_run, 0.f);
+          p.part_ml[part_slot * kM + m] = make_float4(ref_out, l_run, w_run / kPartScale, 0.f);
         else if (p.lse && out_row >= 0)
           p.lse[out_row] = l_run != 0.f ? (ref_out + log2f(l_run)) * 0.69314718055994530942f
                                         : -INFINITY;
