@@ -141,6 +141,22 @@ SPX_API spx_status spx_device_error(int32_t* code, spx_stream stream);
 SPX_API spx_status spx_selftest_wait_timeout(int64_t limit_ns, int64_t* result,
                                              spx_stream stream);
 
+/* The same for the waits that a whole warp makes (the 4-bit attention's): one
+ * CTA of two warps, of which the first waits limit_ns on an mbarrier that
+ * nothing completes, and the second gives up on the first one's abort flag.
+ * The first then makes 16 more waits that cannot succeed as if none had given
+ * up (two suspended attempts of a millisecond at most each), the second 16 as a
+ * kernel does after a timeout (a look each).  The device error word is set
+ * (code 1).
+ *   limit_ns  as above
+ *   result    DEVICE int64 [7]: [0], [1] the warps' waits succeeded (0: they
+ *             gave up), [2], [3] nanoseconds each waited, [4] nanoseconds of
+ *             the first one's later waits, [5] how many of them succeeded,
+ *             [6] nanoseconds of the second one's
+ * Errors as above. */
+SPX_API spx_status spx_selftest_warp_wait_timeout(int64_t limit_ns, int64_t* result,
+                                                  spx_stream stream);
+
 /* ---------------------------------------------------------------------------
  * Step 1 -- IndexPool cache write.  [W1] "IndexPool": k_pool = sum_i w_i k_i,
  * i = 1..4, sum_i w_i = 1, learned w.

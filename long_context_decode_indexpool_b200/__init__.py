@@ -65,6 +65,7 @@ _SIGS = {
     "spx_dims_init": ([_DIMS, _I32, ctypes.c_float], ctypes.c_int),
     "spx_device_error": ([ctypes.POINTER(_I32), _P], ctypes.c_int),
     "spx_selftest_wait_timeout": ([_I64, _P, _P], ctypes.c_int),
+    "spx_selftest_warp_wait_timeout": ([_I64, _P, _P], ctypes.c_int),
     "spx_pool_append": ([_DIMS, _I32, _P, _I32, _P, _P, _P, _I64, _P, _I64, _P], ctypes.c_int),
     "spx_pool_append_tok": ([_DIMS, _I32, _P, _P, _I32, _P, _P, _P, _I64, _P, _I64, _P], ctypes.c_int),
     "spx_index_score": ([_DIMS, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P], ctypes.c_int),
@@ -204,6 +205,12 @@ def spx_selftest_wait_timeout(limit_ns, result, stream=None):
     """Launches the bounded-wait self-test kernel; result: int64 [6] on the device."""
     _check(_lib.spx_selftest_wait_timeout(int(limit_ns), _ptr(result), _stream(stream)),
            "spx_selftest_wait_timeout")
+
+
+def spx_selftest_warp_wait_timeout(limit_ns, result, stream=None):
+    """Launches the self-test of the warp-wide waits; result: int64 [7] on the device."""
+    _check(_lib.spx_selftest_warp_wait_timeout(int(limit_ns), _ptr(result), _stream(stream)),
+           "spx_selftest_warp_wait_timeout")
 
 
 def spx_pool_append(d, B, raw_k, n_new, pool_w, tail, pooled_k, cap_blk, len_dev, max_len,

@@ -133,38 +133,6 @@ __device__ __forceinline__ void pair_sync(int qd) {
   __syncwarp();
   asm volatile("bar.sync %0, 64;" ::"r"(1 + qd) : "memory");
 }
-// Waits for a phase, suspended until it completes (or 1 ms has passed: then the
-// abort flag and the limit of 2^32 - 2^28 clocks, about two seconds, are looked
-// at).  On a timeout it sets the abort flag and the error word.  Every lane of
-// a warp calls it; the result may differ between lanes only after a timeout.
-__device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(addr), "r"(parity), "r"(1000000)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint32_t addr = smem_u32(bar);
-  bool r = true;
-  if (!mbar_try(addr, parity)) {
-    const uint32_t t0 = clock();
-    while (!mbar_try(addr, parity)) {
-      if (*abort || static_cast<uint32_t>(clock()) - t0 > 0xF0000000u) {
-        if (!*abort) atomicExch(&g_device_error, kErrWaitTimeout);
-        *abort = 1;
-        r = false;
-        break;
-      }
-    }
-  }
-  __syncwarp();
-  return r;
-}
 // 16-byte asynchronous copy to shared memory, zeros where `valid` is false; the
 // second makes an mbarrier arrival of the thread's copies so far.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -530,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
   volatile int* const abort = &abort_s;
-  bool ok = true;
+  bool ok = true;  // no wait of this lane gave up
 
   // The items that pass through the slots: for each segment its queries, then
   // its tiles.
@@ -567,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     int seg = 0;  // segments begun
 #pragma unroll 1
     for (int t = 0; t < ntiles;) {
-      ok = __all_sync(0xffffffffu, warp_wait(&bar_raw[slot.i], slot.parity, abort));
+      ok = __all_sync(0xffffffffu, warp_wait(ok, &bar_raw[slot.i], slot.parity, abort));
       if (!ok) break;
       const uint32_t base = slot_u + slot.i * kSlotBytes;
       const int bits = meta_s[slot.i].bits;
@@ -661,11 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       for (int t = 0; t < ntiles; ++t, slot.next()) {
         if (fresh) {
           slot.next();
-          ok &= warp_wait(&bar_q, seg++ & 1, abort);
+          ok = warp_wait(ok, &bar_q, seg & 1, abort);
+          ++seg;
         }
         // S buffer t & 1 is free once the softmax of tile t-2 has read it
-        if (t >= 2) ok &= warp_wait(&bar_p[t & 1], ((t - 2) >> 1) & 1, abort);
-        ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+        if (t >= 2) ok = warp_wait(ok, &bar_p[t & 1], ((t - 2) >> 1) & 1, abort);
+        ok = warp_wait(ok, &bar_full[slot.i], slot.parity, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int bits = meta_s[slot.i].bits;
@@ -688,11 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll 1
       for (int t = 0; t < ntiles; ++t, slot.next()) {
         if (fresh) slot.next();
-        ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+        ok = warp_wait(ok, &bar_full[slot.i], slot.parity, abort);
         const int bits = meta_s[slot.i].bits;
         fresh = (bits & kLast) != 0;
         const int ks = max(1, ((bits & 0xFF) + 15) >> 4);
-        ok &= warp_wait(&bar_p[t & 1], (t >> 1) & 1, abort);
+        ok = warp_wait(ok, &bar_p[t & 1], (t >> 1) & 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -715,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     umma_commit_elect(&bar_drain);
     {
       volatile int no_abort = 0;
-      warp_wait(&bar_drain, 0, &no_abort);
+      warp_wait(true, &bar_drain, 0, &no_abort);
     }
   } else if (warp >= kListWarp) {
     // ======================= list warps =======================================
@@ -783,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       if (round < kSlots)
         ++round;
       else
-        ok = __all_sync(0xffffffffu, ok && warp_wait(&bar_free[slot.i], slot.parity ^ 1u, abort));
+        ok = __all_sync(0xffffffffu, warp_wait(ok, &bar_free[slot.i], slot.parity ^ 1u, abort));
     };
     auto publish = [&](const TileMeta& x) {  // the item of the slot, by lane 0
       if (lane == 0 && lw == 0) {
@@ -858,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
     // the last one's output is still written.  (Thread 4 r + c of a 16 x 256-bit
     // store has columns 2 c, 2 c + 1 of rows r and r + 8.)
     auto take_queries = [&] {
-      ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+      ok = warp_wait(ok, &bar_full[slot.i], slot.parity, abort);
       const float next_hs = hs_s[seg & 3][m];
       ++seg;
 #pragma unroll 1
@@ -903,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 #pragma unroll 1
     for (int t = 0; t < ntiles;) {
       const int buf = t & 1;
-      ok &= warp_wait(&bar_full[slot.i], slot.parity, abort);
+      ok = warp_wait(ok, &bar_full[slot.i], slot.parity, abort);
       // (2^E, E) of this thread's two groups of 8 tokens
       const uint32_t valid = meta_s[slot.i].valid[th];
       uint32_t oc[4];
@@ -913,8 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
                      te_u = smem_u32(&te_s[slot.i][32 * th + 16 * half]);
       slot.next();
       // P buffer t & 1 is free once PV(t-2) is done
-      if (t >= 2) ok &= warp_wait(&bar_pv[buf], ((t - 2) >> 1) & 1, abort);
-      ok &= warp_wait(&bar_qk[buf], (t >> 1) & 1, abort);
+      if (t >= 2) ok = warp_wait(ok, &bar_pv[buf], ((t - 2) >> 1) & 1, abort);
+      ok = warp_wait(ok, &bar_qk[buf], (t >> 1) & 1, abort);
       tc_fence_after();
       uint32_t z[16];  // (floats, in pairs for the paired instructions)
       {
@@ -1029,9 +998,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           // O is scaled in place.  The stores also rewrite the other lanes
           // (queries, logits) with what they hold, so the products in flight
           // are waited for: PV(t-1), and QK(t+1) if the segment goes on.
-          ok &= warp_wait(&bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
+          ok = warp_wait(ok, &bar_pv[(t - 1) & 1], ((t - 1) >> 1) & 1, abort);
           if (t + 1 < seg_end)
-            ok &= warp_wait(&bar_qk[(t + 1) & 1], ((t + 1) >> 1) & 1, abort);
+            ok = warp_wait(ok, &bar_qk[(t + 1) & 1], ((t + 1) >> 1) & 1, abort);
           tc_fence_after();
 #pragma unroll 1
           for (int c = 256 * th; c < 256 * th + 256; c += 32) {
@@ -1072,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
       // The next segment's queries first.  (Both warps of the quarter are behind
       // their last scaling of O, which rewrites the queries' lanes too.)
       if (t < ntiles) hs = take_queries();
-      ok &= warp_wait(&bar_pv[buf], pv_parity, abort);
+      ok = warp_wait(ok, &bar_pv[buf], pv_parity, abort);
       tc_fence_after();
       const float ref_out = m_run == -INFINITY ? -INFINITY : m_run - kLift;
       const bool head = t_org >= 0, whole = head && t_org + tiles <= ntiles;

@@ -72,7 +72,57 @@ __global__ void __launch_bounds__(64, 1) k_wait_selftest(uint64_t limit_ns, int6
   }
 }
 
+// The same for the warp-wide wait: one CTA of two warps.  Warp 0 waits on a
+// barrier that never completes (limit_ns) and gives up; warp 1 waits on another,
+// with a limit 1000 times longer, and gives up on warp 0's abort flag.  Both then
+// make kLateWaits more waits that cannot succeed, warp 0 as one that has not
+// given up yet (two suspended attempts each, then the flag), warp 1 as a kernel's
+// warps do (one look each).
+//   res[0], res[1] the warps' wait results (0: gave up)
+//   res[2], res[3] ns each waited
+//   res[4] ns of warp 0's later waits   res[5] how many of them succeeded (0)
+//   res[6] ns of warp 1's later waits
+constexpr int kLateWaits = 16;
+
+__global__ void __launch_bounds__(64, 1) k_warp_wait_selftest(uint64_t limit_ns, int64_t* res) {
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  volatile int* abort = &abort_flag;
+  uint64_t t0 = globaltimer_ns();
+  bool ok = warp_wait(true, &bars[warp], 0, abort, warp == 0 ? limit_ns : limit_ns * 1000ull);
+  if (lane == 0) {
+    res[warp] = ok ? 1 : 0;
+    res[2 + warp] = static_cast<int64_t>(globaltimer_ns() - t0);
+  }
+  __syncwarp();
+  t0 = globaltimer_ns();
+  int late = 0;
+  for (int i = 0; i < kLateWaits; ++i) {
+    if (warp == 0) {
+      late += warp_wait(true, &bars[0], 0, abort) ? 1 : 0;
+    } else {
+      ok = warp_wait(ok, &bars[1], 0, abort);
+    }
+  }
+  if (lane == 0) res[warp == 0 ? 4 : 6] = static_cast<int64_t>(globaltimer_ns() - t0);
+  if (threadIdx.x == 0) res[5] = late;
+}
+
 }  // namespace
+
+cudaError_t launch_warp_wait_selftest(uint64_t limit_ns, int64_t* res, cudaStream_t stream) {
+  k_warp_wait_selftest<<<1, 64, 0, stream>>>(limit_ns, res);
+  count_launches(1);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int64_t* res, cudaStream_t stream) {
   k_wait_selftest<<<1, 64, 0, stream>>>(limit_ns, res);

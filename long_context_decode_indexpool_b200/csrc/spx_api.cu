@@ -336,6 +336,13 @@ spx_status spx_selftest_wait_timeout(int64_t limit_ns, int64_t* result, spx_stre
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
+spx_status spx_selftest_warp_wait_timeout(int64_t limit_ns, int64_t* result, spx_stream stream) {
+  if (!result || (reinterpret_cast<uintptr_t>(result) & 7)) return SPX_ERR_INVALID_ARG;
+  if (limit_ns < 1000 || limit_ns > 1000000000) return SPX_ERR_INVALID_ARG;
+  return cuda_status(launch_warp_wait_selftest(static_cast<uint64_t>(limit_ns), result,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // ---------------------------------------------------------------------------
 }  // extern "C"
 

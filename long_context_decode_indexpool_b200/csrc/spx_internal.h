@@ -258,9 +258,10 @@ struct WsArgs {
 };
 cudaError_t launch_ws_update(const WsArgs& a, cudaStream_t stream);
 
-// Self-test of the bounded waits (one CTA; see selftest.cu).  res: device
-// int64 [6].
+// Self-tests of the bounded waits (one CTA; see selftest.cu).  res: device
+// int64 [6]; [7] for the warp-wide form.
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int64_t* res, cudaStream_t stream);
+cudaError_t launch_warp_wait_selftest(uint64_t limit_ns, int64_t* res, cudaStream_t stream);
 
 // Tensor-map encoding through the driver entry point (no libcuda link).
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank,
