@@ -34,7 +34,6 @@ spx_status attn_fp4(const spx_dims* d, int32_t rows, int32_t per_seq, const void
   if (p.tiles > 0x7fffffff) return SPX_ERR_UNSUPPORTED;
   if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes || !al(ws, 16))) return SPX_ERR_WORKSPACE;
   AttnFp4Args a{};
-  a.rows = rows;
   a.per_seq = per_seq;
   a.heads = d->heads;
   a.q = q;

@@ -209,7 +209,7 @@ struct AttnFp4Plan {
   size_t ws_bytes;
 };
 struct AttnFp4Args {
-  int rows, per_seq, heads;  // row r attends to sequence r / per_seq
+  int per_seq, heads;    // row r attends to sequence r / per_seq
   const void* q;
   const uint8_t* codes;
   const uint8_t* scales;

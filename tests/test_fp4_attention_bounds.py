@@ -6,7 +6,8 @@ import torch
 
 import oracle
 import synth
-from _gpu_helpers import need_gpu, to_dev_bf16
+from _gpu_helpers import LSE_ATOL, assert_attention_close, need_gpu, to_dev_bf16
+from test_fp4_latent import _run_latent, _run_sparse, _sparse_inputs, _tokens
 
 FAKE = 1 << 20  # an aligned non-null address; never dereferenced
 
@@ -83,3 +84,30 @@ def test_no_bound_is_the_cache_s_own(rows):
         got.append((out, lse))
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+# ---------------------------------------------------------------------------
+# against the oracle's own attention (C++, fp64)
+# ---------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,n_vis", [(16, [1, 700]), (64, [2049, 130]), (80, [63, 1027])])
+def test_against_the_oracle_s_attention(heads, n_vis):
+    spx = need_gpu()
+    rng = np.random.default_rng(heads)
+    d, cap = spx.dims(heads, 0.8), max(n_vis)
+    codes, scales = oracle.latent_fp4(
+        synth.f32_to_bf16_bits_np(rng.standard_normal((2 * cap, 512)).astype(np.float32)))
+    codes, scales = codes.reshape(2, cap, 256), scales.reshape(2, cap, 16)
+    qb = synth.f32_to_bf16_bits_np((rng.standard_normal((2, heads, 512)) / 22).astype(np.float32))
+    dev = [torch.from_numpy(a).cuda() for a in (codes, scales)]
+    n_dev = torch.tensor(n_vis, dtype=torch.int64, device="cuda")
+    got, lse = _run_latent(spx, d, 1, to_dev_bf16(qb), *dev, n_dev, cap)
+    idx, cnt = _sparse_inputs(rng, n_vis, spoil=False)
+    sp, sp_lse = _run_sparse(spx, d, to_dev_bf16(qb), *dev, cap * 512, cap,
+                             torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(), n_dev, cap)
+    for r, n in enumerate(n_vis):
+        pos = _tokens(idx[r], cnt[r], n)
+        for o, l, rows in ((got[r], lse[r], slice(0, n)), (sp[r], sp_lse[r], pos)):
+            ref, ref_lse = oracle.attention_fp4(qb[r], codes[r][rows], scales[r][rows], 0.8)
+            assert_attention_close(o, ref, f"row {r}")
+            assert np.abs(l - ref_lse).max() <= LSE_ATOL
