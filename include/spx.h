@@ -404,7 +404,8 @@ SPX_API spx_status spx_sparse_mla_attn_fp8(const spx_dims* d, int32_t rows, cons
  * stays the same from 2^31 - 1 on).
  *
  * A row that sees no token gives out = 0 and lse = -inf; one that sees a NaN
- * group gives NaN, the others do not.  The queries are expected to be finite.
+ * group gives NaN, the others do not.  The queries are expected to be finite,
+ * and so, in fp32, a logit's sum of absolute terms times log2(e).
  * The cache arrays may be pinned host memory mapped into the device's address
  * space.  A workspace belongs to one call at a time; calls that may overlap on
  * the GPU need one each.

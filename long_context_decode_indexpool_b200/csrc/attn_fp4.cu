@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
           factors(i, f, e);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            z[i + k] = __float_as_uint(fmaf(__uint_as_float(z[i + k]) * hs, __uint_as_float(f[k]),
+            z[i + k] = __float_as_uint(fmaf(__uint_as_float(z[i + k]), hs * __uint_as_float(f[k]),
                                             __uint_as_float(e[k])));
         }
       }

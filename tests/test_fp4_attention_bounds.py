@@ -111,3 +111,36 @@ def test_against_the_oracle_s_attention(heads, n_vis):
             ref, ref_lse = oracle.attention_fp4(qb[r], codes[r][rows], scales[r][rows], 0.8)
             assert_attention_close(o, ref, f"row {r}")
             assert np.abs(l - ref_lse).max() <= LSE_ATOL
+
+
+# ---------------------------------------------------------------------------
+# the largest queries
+# ---------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("low,high", [(-50, -50), (-50, -44), (-50, -30)])
+def test_largest_queries_over_small_rows(low, high):
+    """Queries near bf16's largest value and rows near the format's smallest: logits of
+    about 2^80 (finite in fp32), so the softmax picks one token.  Rows alike in size, and
+    rows whose 8 neighbours cannot share an exponent."""
+    spx = need_gpu()
+    rng = np.random.default_rng(65 - low + high)
+    n, heads = 150, 16
+    x = rng.standard_normal((n, 512)) * np.exp2(rng.choice([low, high], (n, 1)).astype(float))
+    codes, scales = oracle.latent_fp4(synth.f32_to_bf16_bits_np(x.astype(np.float32)))
+    vals = oracle.dequant_fp4(codes, scales)
+    qb = synth.f32_to_bf16_bits_np((rng.standard_normal((1, heads, 512)) * 2.0 ** 124)
+                                   .astype(np.float32))
+    q = oracle.bf16_to_f64(qb)[0]
+    z = q @ vals.T
+    best = z.argmax(-1)
+    top2 = np.sort(z, -1)[:, -2:]
+    # the terms' absolute sum times 512 * 2^-23 (a sum of 512 products in fp32) is below
+    # the lead of the best token, which is of 2^60 bits and more
+    assert (top2[:, 1] - top2[:, 0] > 2.0 ** -14 * (np.abs(q) @ np.abs(vals).T).max(-1)).all()
+    d = spx.dims(heads, 1.0)
+    got, lse = _run_latent(spx, d, 1, to_dev_bf16(qb), torch.from_numpy(codes)[None].cuda(),
+                           torch.from_numpy(scales)[None].cuda(),
+                           torch.tensor([n], dtype=torch.int64, device="cuda"), n)
+    assert np.array_equal(got[0], vals[best])
+    assert (np.abs(lse[0] - top2[:, 1]) <= 2.0 ** -13 * np.abs(q).max() * 512 * np.abs(vals).max()).all()
+    assert np.isfinite(lse).all()
