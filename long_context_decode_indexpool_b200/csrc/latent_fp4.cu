@@ -88,8 +88,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // A warp takes kRows rows in a row, all of whose loads it issues first: 1 where
-// there are few rows, 4 where there are many (131,056 rows: 30.4 us with one,
-// 26.6 with four).
+// there are few rows, 4 where there are many (many_rows below).
 template <int kRows>
 __global__ void __launch_bounds__(kThreads)
     k_latent_read_fp4(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -134,8 +133,12 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Rows from which a warp reads 4: as many as fill the 64 warps of 148 SMs then.
-constexpr int64_t kManyRows = 4 * 148 * 64;
+// Whether a warp reads 4 rows: from as many on as give half of the device's warps
+// (64 an SM) work then.  Measured, one row a warp / four, on 148 SMs (18,944 rows),
+// in us, rows from the front: 4,096 rows 2.7 / 3.0, 16,384 6.5 / 6.7, 24,576
+// 8.4 / 8.1, 131,072 32.1 / 29.0; scattered rows: 4,096 2.9 / 3.4, 16,384 7.0 /
+// 6.9, 24,576 8.8 / 8.4, 131,072 35.8 / 27.3.
+bool many_rows(int64_t rows) { return rows >= int64_t(2) * 64 * device_sm_count(); }
 
 cudaError_t grid_for(int64_t rows, int per_warp, unsigned* grid) {
   const int64_t per = kThreads / 32 * per_warp;
@@ -167,7 +170,7 @@ cudaError_t launch_latent_read_fp4(int B, const uint8_t* codes, const uint8_t* s
                                    const int64_t* n_vis, void* out, cudaStream_t stream) {
   const int64_t rows = B * m;
   if (rows <= 0) return cudaSuccess;
-  const bool many = rows >= kManyRows;
+  const bool many = many_rows(rows);
   unsigned grid = 0;
   if (cudaError_t e = grid_for(rows, many ? 4 : 1, &grid)) return e;
   auto* kernel = many ? k_latent_read_fp4<4> : k_latent_read_fp4<1>;

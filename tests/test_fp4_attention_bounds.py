@@ -144,3 +144,33 @@ def test_largest_queries_over_small_rows(low, high):
     assert np.array_equal(got[0], vals[best])
     assert (np.abs(lse[0] - top2[:, 1]) <= 2.0 ** -13 * np.abs(q).max() * 512 * np.abs(vals).max()).all()
     assert np.isfinite(lse).all()
+
+
+# ---------------------------------------------------------------------------
+# the read back's two forms
+# ---------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("more", [-1, 0, 1, 2, 3])
+@pytest.mark.parametrize("scattered", [False, True])
+def test_read_back_where_its_form_changes(more, scattered):
+    """A call of about 128 rows an SM gives what calls of fewer rows give."""
+    spx = need_gpu()
+    m = 128 * torch.cuda.get_device_properties(0).multi_processor_count + more
+    g = torch.Generator(device="cuda").manual_seed(m)
+    cap, n = m + 5, m - 7  # the last rows lie behind the sequence's end
+    codes = torch.randint(0, 256, (1, cap, 256), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(100, 140, (1, cap, 16), dtype=torch.uint8, device="cuda", generator=g)
+    n_vis = torch.tensor([n], device="cuda")
+    pos = torch.arange(m, device="cuda")[None]
+    if scattered:
+        pos = torch.randint(-3, cap + 3, (1, m), device="cuda", generator=g)
+    out = torch.full((1, m, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    spx.spx_latent_read_fp4(1, codes, scales, cap, pos if scattered else None, m, n_vis, out)
+    ref = torch.full_like(out, 5.0)
+    for at in range(0, m, 5000):
+        k = min(5000, m - at)
+        spx.spx_latent_read_fp4(1, codes, scales, cap, pos[:, at:].contiguous(), k, n_vis,
+                                ref[:, at:])
+    assert torch.equal(out, ref)
+    seen = (pos >= 0) & (pos < n)
+    assert (out[~seen] == 0).all() and (out[seen] != 0).any(-1).all()
