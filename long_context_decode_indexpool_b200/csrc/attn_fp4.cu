@@ -1122,10 +1122,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const KParams p) {
 // Joins the parts of the units that several CTAs shared.  Block (c, y) takes the
 // unit whose first part CTA c left and an equal share of its pieces of 8 dims;
 // a thread a piece, in one pass over the parts with a running R (a part's loads
-// then wait for nothing but the unit's record).  With few units the shares are
-// small (many blocks, many loads in flight), with many they are larger (fewer
-// blocks that find nothing to do).
+// then wait for nothing but the unit's record).
 constexpr int kJoinThreads = 256;
+// Shares of a unit: many with few units (many loads in flight), fewer with many
+// (fewer blocks that find nothing to do).  Measured, whole call, 16 / 8 / 4 shares,
+// in us: 1 row of 64 heads over 8,192 tokens 27.7 / 37.2 / 57.0, 31 such rows 84.0 /
+// 82.0 / 85.5, 48 114.5 / 114.2 / 113.7; 16 heads over 2,051 tokens, 31 rows 33.6 /
+// 34.8 / 39.3, 32 36.1 / 36.3 / 40.0, 64 51.1 / 49.7 / 51.7, 256 144.9 / 142.3 / 143.2.
+constexpr int kJoinFew = 32;  // units
+constexpr int join_shares(int units) { return units < kJoinFew ? 16 : 8; }
 template <bool kSparse>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_fp4_combine(const KParams p) {
   pdl_trigger();
@@ -1199,7 +1204,7 @@ cudaError_t launch(const AttnFp4Plan& pl, const KParams& p, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (pl.ws_bytes > 0) {
-    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, pl.units < 32 ? 16 : 4),
+    e = launch_ex(k_attn_fp4_combine<kSparse>, dim3(pl.grid, join_shares(pl.units)),
                   dim3(kJoinThreads), 0, stream,
                   true, 1, p);
     if (e != cudaSuccess) return e;

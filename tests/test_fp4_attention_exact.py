@@ -168,7 +168,8 @@ def test_whole_cache_counts_every_token_once(heads, case, spread):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("seqs,per,cap,heads", [(613, 1, 70, 16), (300, 3, 200, 80), (1, 200, 900, 64),
-                                                (2, 129, 1300, 16)])
+                                                (2, 129, 1300, 16), (31, 1, 600, 64),
+                                                (32, 1, 600, 64), (33, 1, 600, 16)])
 def test_many_units_count_every_token_once(seqs, per, cap, heads):
     """Many short sequences, and chunks of many rows over one cache, each row with its
     own (causal, or any) length."""
