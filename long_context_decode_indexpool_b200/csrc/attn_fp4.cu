@@ -60,6 +60,7 @@
 #include "spx_device.cuh"
 #include "spx_internal.h"
 #include "spx_launch.cuh"
+#include "spx_warp_wait.cuh"
 
 namespace spx {
 

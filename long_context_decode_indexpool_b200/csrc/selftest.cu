@@ -7,6 +7,7 @@
 // or a hang: every wait here is bounded.
 #include "spx_device.cuh"
 #include "spx_internal.h"
+#include "spx_warp_wait.cuh"
 
 namespace spx {
 

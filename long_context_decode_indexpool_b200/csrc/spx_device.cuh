@@ -110,43 +110,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
-// The same wait made by every lane of a warp, suspended for up to a millisecond
-// at a time (the waiting warps of a CTA then leave the issue slots to the working
-// ones).  `ok` is the lane's last answer: a lane whose wait gave up looks at later
-// barriers once, without suspending, so what is left of its warp's work waits for
-// nothing more.  The lanes' answers may differ only after a timeout.  (A branch
-// around that look cost the 4-bit attention registers: a chunk of 1,024
-// selections took 495 us, 480 so.)
-__device__ __forceinline__ bool mbar_try_wait_for(uint32_t addr, uint32_t parity, uint32_t ns) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(addr), "r"(parity), "r"(ns)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool warp_wait(bool ok, uint64_t* bar, uint32_t parity,
-                                          volatile int* abort, uint64_t limit_ns = kWaitLimitNs) {
-  constexpr uint32_t kSuspendNs = 1000000;
-  const uint32_t addr = smem_u32(bar);
-  if (!mbar_try_wait_for(addr, parity, ok ? kSuspendNs : 0) && ok) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_for(addr, parity, kSuspendNs)) {
-      if (*abort || globaltimer_ns() - t0 > limit_ns) {
-        if (!*abort) atomicExch(&g_device_error, kErrWaitTimeout);
-        *abort = 1;
-        ok = false;
-        break;
-      }
-    }
-  }
-  __syncwarp();
-  return ok;
-}
-
 // ---------------------------------------------------------------------------
 // TMA tile loads (one CTA each)
 // ---------------------------------------------------------------------------
