@@ -494,6 +494,9 @@ SPX_API spx_status spx_sparse_mla_attn_ws(const spx_dims* d, int32_t rows, const
  *   timing    optional events around the scoring launch (may be NULL); the
  *             kernels of the call may otherwise start before their
  *             predecessor in the call has finished (they wait for its data)
+ * The attention's queries are fetched ahead of those waits: q must not be an
+ * output (out) of the attention call right before this one on the stream
+ * unless another kernel of the caller's stands between the two.
  * ------------------------------------------------------------------------- */
 SPX_API spx_status spx_decode_workspace_size(const spx_dims* d, int32_t B,
                                      int64_t max_len, size_t* bytes);

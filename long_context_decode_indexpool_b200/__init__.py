@@ -5,9 +5,9 @@ function here has the C function's name and arguments, takes torch tensors
 where the C call takes device pointers, passes ``tensor.data_ptr()`` and the
 current CUDA stream, and raises ``SpxError`` on a non-zero status.  All
 computation happens in the library's CUDA kernels; torch only provides device
-memory and streams.  The tensors of a call lie on the current device (or in
-pinned host memory where the header allows it).  There is no fallback: if
-``libspx.so`` is missing the import fails.
+memory and streams.  The tensors of a call are contiguous and lie on the
+current device (or in pinned host memory where the header allows it).  There is
+no fallback: if ``libspx.so`` is missing the import fails.
 """
 from __future__ import annotations
 

@@ -43,14 +43,14 @@
 // (256-383), lanes 16-31 O (0-511).
 //
 // What bounds it.  An M = 64 product runs at half the tensor rate (2,048 cycles
-// a tile: 0.36 ms for four sequences of 0.5-1M tokens, where it takes 0.57); a
+// a tile: 0.36 ms for four sequences of 0.5-1M tokens, where it takes 0.65); a
 // tile's operand reads (1,130 wavefronts of 128 bytes: the queries in TMEM save
 // 512), its expansion and copies (about 1,300) share one shared-memory port;
 // and a slot's round (copy, expand, QK, softmax, PV: about 10,000 cycles with
-// three in flight) sets the pace at 3,400 cycles a tile.  Where units are short,
+// three in flight) sets the pace at 3,500 cycles a tile.  Where units are short,
 // their joints count: the next unit's queries go to TMEM before the last one's
 // output is read from it, so that its first products run meanwhile (1,024 units
-// of 33 tiles: 497 us with the output first, 476 so).  Tried and slower: two
+// of 33 tiles: 497 us with the output first, 479 so).  Tried and slower: two
 // slots and the queries in shared memory (4,200); the converters loading their
 // own rows into registers (3,800); bulk copies of 1 KiB blocks (the copy
 // engine takes 75 cycles each: 5,600); 16 warps with one list for all (5,000).
